@@ -40,8 +40,9 @@ extern "C" {
 typedef enum {
   SQ_OK = 0,
   SQ_E_NULL = 1,      /* a required pointer is NULL                               */
-  SQ_E_SHAPE = 2,     /* K % 256 != 0, K < 256, N < 1 or M < 0; the input         */
-                      /* gradient also needs N % 64 == 0                          */
+  SQ_E_SHAPE = 2,     /* K % 256 != 0, K < 256, N < 1 or M < 0; the W4 input      */
+                      /* gradient also needs N % 64 == 0; the 8-bit products      */
+                      /* have upper limits (stated there) and need groups >= 1    */
   SQ_E_GROUP = 3,     /* group is not 32 or 64                                    */
   SQ_E_RANK = 4,      /* rank is not 0, 32 or 64 (the int8 and MXFP4 modes also  */
                       /* take 16); see the note on ranks below                    */
@@ -243,6 +244,64 @@ size_t sq_linear_fwd_w8_workspace_bytes(int64_t m, const sq_w8_t *p);
 sq_status_t sq_linear_fwd_w8(const uint16_t *x, int64_t m, const sq_w8_t *p, void *y,
                              sq_dtype_t y_dtype, void *workspace, size_t workspace_bytes,
                              void *stream);
+
+/* 8-bit forward of an int8-mode payload (W8A8: 8-bit tokens, 8-bit weights;
+ * half the matrix time of sq_linear_fwd_w8, with the error of 8-bit tokens):
+ *   y[m][n] = s[m] * p->scales[n] * sum_k q[m][k] * codes[n][k]
+ *           + sum_r (x @ lora_down)[m][r] lora_up[n][r]
+ * with q and s the 8-bit integers and the scale of row m of x @ H:
+ *   each block of 256 values with absmax below 2^e (e as small as that allows,
+ *   at least -125) is held as integers X = trunc(x 2^(23 - e)); R = X S with S
+ *   the +-1 Sylvester matrix, exact in int32; r = fp32(R) 2^(e - 27);
+ *   a = max(max_k |r|, 2^-100); s = fp32(a / 127); i = fp32(127 / a);
+ *   q = round_half_even(fp32(r i)), |q| <= 127.
+ * Every step is one correctly rounded operation, so q and s depend on the row
+ * alone.  The integer sum is exact; the scales and the rank-r term (t = x @
+ * lora_down summed in fp32, carried as bf16 hi + lo) are applied in fp32.  A
+ * row of x that holds inf or NaN gives a row of NaN and touches no other row.
+ * x bf16 [m][k], y fp32 or bf16 [m][n] (bf16 = RNE of the fp32 result).
+ * K <= 65536 (SQ_E_SHAPE).  `workspace`: caller-owned device scratch of at
+ * least sq_linear_fwd_w8a8_workspace_bytes(m, p) bytes (0 for unsupported
+ * shapes), not read before it is written; m == 0 is a no-op. */
+size_t sq_linear_fwd_w8a8_workspace_bytes(int64_t m, const sq_w8_t *p);
+sq_status_t sq_linear_fwd_w8a8(const uint16_t *x, int64_t m, const sq_w8_t *p, void *y,
+                               sq_dtype_t y_dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* Input gradient of the int8 mode (dx = dy @ W_hat; the backward of both
+ * int8-mode forwards, the tokens' rounding passed straight through):
+ *   dx = (t / 16) * ((d @ codes) S) + (dy @ lora_up) @ lora_down^T
+ * with d and t the 16-bit integers and the scale of each row of
+ * v = fp32(dy[m][n] * scales[n]):
+ *   a = max(max_n |v|, 2^-100); t = fp32(a / 32512); i = fp32(32512 / a);
+ *   d = round_half_even(fp32(v i)), |d| <= 32512,
+ * that is a step of 2^-15 of the row's largest value.  d @ codes is exact in
+ * integers; the rest is fp32.  A row that holds inf or NaN gives a row of NaN
+ * and touches no other row.  dy bf16 [m][n], dx fp32 or bf16 [m][k].  Any
+ * N <= 131072 (no multiple needed), K <= 65536.  Workspace and m == 0 as above. */
+size_t sq_linear_dgrad_w8_workspace_bytes(int64_t m, const sq_w8_t *p);
+sq_status_t sq_linear_dgrad_w8(const uint16_t *dy, int64_t m, const sq_w8_t *p, void *dx,
+                               sq_dtype_t dx_dtype, void *workspace, size_t workspace_bytes,
+                               void *stream);
+
+/* The two calls above over several experts: `groups` int8-mode payloads of one
+ * shape, stacked in p (codes [groups][n][k], scales [groups][n], lora_up
+ * [groups][n][rank], lora_down [groups][k][rank]; p->n and p->k are one
+ * expert's).  Rows are sorted by expert: expert e takes rows
+ * offsets[e] .. offsets[e+1]-1 of x and y (dy and dx).  offsets is a device
+ * array of groups + 1 nondecreasing int32, read when the kernels run, so a
+ * captured graph follows new contents.  An expert may have no rows.  Rows
+ * before offsets[0] and from offsets[groups] on are left as they were.  Each
+ * value is clamped into [0, m] on the device, so wrong offsets give wrong
+ * rows but no access outside the tensors.  groups >= 1, m < 2^31. */
+size_t sq_grouped_fwd_w8a8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t *p);
+sq_status_t sq_grouped_fwd_w8a8(const uint16_t *x, int64_t m, const int32_t *offsets,
+                                int32_t groups, const sq_w8_t *p, void *y, sq_dtype_t y_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+size_t sq_grouped_dgrad_w8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t *p);
+sq_status_t sq_grouped_dgrad_w8(const uint16_t *dy, int64_t m, const int32_t *offsets,
+                                int32_t groups, const sq_w8_t *p, void *dx, sq_dtype_t dx_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------------
  * MXFP4 mode (SquareQ README, "SquareQ v3 - W4", the "Residual codecs"

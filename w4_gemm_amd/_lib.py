@@ -25,7 +25,11 @@ EXPORTS = ("sq_quantize_weight", "sq_linear_fwd_workspace_bytes", "sq_linear_fwd
            "sq_abi_version", "sq_quantize_weight_w8_workspace_bytes", "sq_quantize_weight_w8",
            "sq_reconstruct_bf16_w8", "sq_linear_fwd_w8_workspace_bytes", "sq_linear_fwd_w8",
            "sq_quantize_weight_mx4", "sq_quantize_act_mx4", "sq_reconstruct_bf16_mx4",
-           "sq_linear_fwd_mx4_workspace_bytes", "sq_linear_fwd_mx4", "sq_linear_fwd_static")
+           "sq_linear_fwd_mx4_workspace_bytes", "sq_linear_fwd_mx4", "sq_linear_fwd_static",
+           "sq_linear_fwd_w8a8_workspace_bytes", "sq_linear_fwd_w8a8",
+           "sq_linear_dgrad_w8_workspace_bytes", "sq_linear_dgrad_w8",
+           "sq_grouped_fwd_w8a8_workspace_bytes", "sq_grouped_fwd_w8a8",
+           "sq_grouped_dgrad_w8_workspace_bytes", "sq_grouped_dgrad_w8")
 SQ_FWD_STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -120,6 +124,20 @@ def lib() -> ctypes.CDLL:
         L.sq_linear_fwd_w8_workspace_bytes.restype = ctypes.c_size_t
         L.sq_linear_fwd_w8.argtypes = [vp, i64, P8, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
         L.sq_linear_fwd_w8.restype = ctypes.c_int
+        for name in ("sq_linear_fwd_w8a8", "sq_linear_dgrad_w8"):
+            f = getattr(L, name)
+            f.argtypes = [vp, i64, P8, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
+            f.restype = ctypes.c_int
+            f = getattr(L, name + "_workspace_bytes")
+            f.argtypes = [i64, P8]
+            f.restype = ctypes.c_size_t
+        for name in ("sq_grouped_fwd_w8a8", "sq_grouped_dgrad_w8"):
+            f = getattr(L, name)
+            f.argtypes = [vp, i64, vp, i32, P8, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
+            f.restype = ctypes.c_int
+            f = getattr(L, name + "_workspace_bytes")
+            f.argtypes = [i64, i32, P8]
+            f.restype = ctypes.c_size_t
         PX = ctypes.POINTER(SqMx4)
         L.sq_quantize_weight_mx4.argtypes = [vp, PX, vp, vp]
         L.sq_quantize_weight_mx4.restype = ctypes.c_int
@@ -211,6 +229,46 @@ def sq_linear_fwd_w8(x, m: int, p: SqW8, y, y_dtype: int, workspace, workspace_b
                      stream) -> int:
     return lib().sq_linear_fwd_w8(x, m, ctypes.byref(p), y, y_dtype, workspace, workspace_bytes,
                                   stream)
+
+
+def sq_linear_fwd_w8a8_workspace_bytes(m: int, p: SqW8) -> int:
+    return lib().sq_linear_fwd_w8a8_workspace_bytes(m, ctypes.byref(p))
+
+
+def sq_linear_fwd_w8a8(x, m: int, p: SqW8, y, y_dtype: int, workspace, workspace_bytes: int,
+                       stream) -> int:
+    return lib().sq_linear_fwd_w8a8(x, m, ctypes.byref(p), y, y_dtype, workspace,
+                                    workspace_bytes, stream)
+
+
+def sq_linear_dgrad_w8_workspace_bytes(m: int, p: SqW8) -> int:
+    return lib().sq_linear_dgrad_w8_workspace_bytes(m, ctypes.byref(p))
+
+
+def sq_linear_dgrad_w8(dy, m: int, p: SqW8, dx, dx_dtype: int, workspace, workspace_bytes: int,
+                       stream) -> int:
+    return lib().sq_linear_dgrad_w8(dy, m, ctypes.byref(p), dx, dx_dtype, workspace,
+                                    workspace_bytes, stream)
+
+
+def sq_grouped_fwd_w8a8_workspace_bytes(m: int, groups: int, p: SqW8) -> int:
+    return lib().sq_grouped_fwd_w8a8_workspace_bytes(m, groups, ctypes.byref(p))
+
+
+def sq_grouped_fwd_w8a8(x, m: int, offsets, groups: int, p: SqW8, y, y_dtype: int, workspace,
+                        workspace_bytes: int, stream) -> int:
+    return lib().sq_grouped_fwd_w8a8(x, m, offsets, groups, ctypes.byref(p), y, y_dtype,
+                                     workspace, workspace_bytes, stream)
+
+
+def sq_grouped_dgrad_w8_workspace_bytes(m: int, groups: int, p: SqW8) -> int:
+    return lib().sq_grouped_dgrad_w8_workspace_bytes(m, groups, ctypes.byref(p))
+
+
+def sq_grouped_dgrad_w8(dy, m: int, offsets, groups: int, p: SqW8, dx, dx_dtype: int, workspace,
+                        workspace_bytes: int, stream) -> int:
+    return lib().sq_grouped_dgrad_w8(dy, m, offsets, groups, ctypes.byref(p), dx, dx_dtype,
+                                     workspace, workspace_bytes, stream)
 
 
 def sq_quantize_weight_mx4(w, p: SqMx4, dev_flags, stream) -> int:

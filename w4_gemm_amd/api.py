@@ -290,6 +290,146 @@ def linear_fwd_w8(x: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
     return out
 
 
+# ---------------------------------------------------------------- 8-bit products
+@dataclass
+class GroupedW8Payload:
+    """Device tensors of E int8-residual layers of one shape (one per expert), stacked."""
+    codes: torch.Tensor      # int8 [E, N, K]
+    scales: torch.Tensor     # float16 [E, N]
+    up: torch.Tensor | None  # bfloat16 [E, N, rank]
+    down: torch.Tensor | None  # bfloat16 [E, K, rank]
+
+    @property
+    def groups(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def n(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def k(self) -> int:
+        return self.codes.shape[2]
+
+    @property
+    def rank(self) -> int:
+        return 0 if self.up is None else self.up.shape[2]
+
+    def abi(self) -> SqW8:
+        _require(self.codes, torch.int8, "codes")
+        _require(self.scales, torch.float16, "scales")
+        S.check_grouped_w8_payload(self.codes.shape, self.scales.shape, _shp(self.up),
+                                   _shp(self.down))
+        if self.up is not None:
+            _require(self.up, torch.bfloat16, "up")
+            _require(self.down, torch.bfloat16, "down")
+        return SqW8(self.n, self.k, self.rank, 0, _ptr(self.codes), _ptr(self.scales),
+                    _ptr(self.up), _ptr(self.down))
+
+
+def stack_payloads_w8(payloads) -> GroupedW8Payload:
+    """One GroupedW8Payload from the int8-residual payloads of experts 0, 1, ... (copies)."""
+    payloads = list(payloads)
+    if not payloads:
+        raise ValueError("need at least one payload")
+    first = payloads[0]
+    for p in payloads:
+        if (p.n, p.k, p.rank) != (first.n, first.k, first.rank):
+            raise ValueError("every expert must have the same N, K and rank")
+    return GroupedW8Payload(
+        torch.stack([p.codes for p in payloads]), torch.stack([p.scales for p in payloads]),
+        torch.stack([p.up for p in payloads]) if first.rank else None,
+        torch.stack([p.down for p in payloads]) if first.rank else None)
+
+
+def _on_current_device(*tensors):
+    """Refuse tensors of another device than the one the kernels would run on."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise ValueError(f"tensors must live on the current device (cuda:{cur}), "
+                             f"got {t.device}")
+
+
+def _i8_product(name, a, cols_in, cols_out, p, offsets, out_dtype, workspace, out, in_name):
+    """The common part of the four 8-bit products (checks, allocation, call)."""
+    _require(a, torch.bfloat16, in_name)
+    m = S.check_rows(in_name, a.shape, cols_in)
+    abi = p.abi()
+    if out is None:
+        if out_dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+        out = torch.empty((m, cols_out), dtype=out_dtype, device=a.device)
+    _require(out, out.dtype, "out")
+    if out.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("out must be fp32 or bf16")
+    S.check_out("out", out.shape, (m, cols_out))
+    dt = SQ_BF16 if out.dtype == torch.bfloat16 else SQ_F32
+    if offsets is None:
+        nbytes = getattr(_lib, name + "_workspace_bytes")(m, abi)
+    else:
+        _require(offsets, torch.int32, "offsets")
+        S.check_offsets(offsets.shape, p.groups)
+        nbytes = getattr(_lib, name + "_workspace_bytes")(m, p.groups, abi)
+    if workspace is None:
+        workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=a.device)
+    _on_current_device(a, p.codes, p.scales, p.up, p.down, offsets, out, workspace)
+    tail = (abi, out.data_ptr(), dt, workspace.data_ptr(), _nbytes(workspace), _stream())
+    if offsets is None:
+        _check(getattr(_lib, name)(a.data_ptr(), m, *tail), name)
+    else:
+        _check(getattr(_lib, name)(a.data_ptr(), m, offsets.data_ptr(), p.groups, *tail), name)
+    return out
+
+
+def fwd_w8a8_workspace_bytes(m: int, p: W8Payload) -> int:
+    return _lib.sq_linear_fwd_w8a8_workspace_bytes(m, p.abi())
+
+
+def linear_fwd_w8a8(x: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_linear_fwd_w8a8: bf16 x [M,K] -> y [M,N] (fp32 or bf16), 8-bit tokens and weights."""
+    return _i8_product("sq_linear_fwd_w8a8", x, p.k, p.n, p, None, out_dtype, workspace, out, "x")
+
+
+def dgrad_w8_workspace_bytes(m: int, p: W8Payload) -> int:
+    return _lib.sq_linear_dgrad_w8_workspace_bytes(m, p.abi())
+
+
+def linear_dgrad_w8(dy: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_linear_dgrad_w8: bf16 dy [M,N] -> dx = dy @ W_hat [M,K] (fp32 or bf16)."""
+    return _i8_product("sq_linear_dgrad_w8", dy, p.n, p.k, p, None, out_dtype, workspace, out,
+                       "dy")
+
+
+def grouped_fwd_w8a8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
+    return _lib.sq_grouped_fwd_w8a8_workspace_bytes(m, p.groups, p.abi())
+
+
+def grouped_fwd_w8a8(x: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payload,
+                     out_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None):
+    """sq_grouped_fwd_w8a8: rows offsets[e]..offsets[e+1]-1 of x [M,K] through expert e.
+
+    offsets is an int32 device tensor [E+1]; rows outside the experts' ranges are left as they
+    were in `out` (undefined when it is allocated here)."""
+    return _i8_product("sq_grouped_fwd_w8a8", x, p.k, p.n, p, offsets, out_dtype, workspace, out,
+                       "x")
+
+
+def grouped_dgrad_w8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
+    return _lib.sq_grouped_dgrad_w8_workspace_bytes(m, p.groups, p.abi())
+
+
+def grouped_dgrad_w8(dy: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payload,
+                     out_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None):
+    """sq_grouped_dgrad_w8: the input gradient of grouped_fwd_w8a8, rows and offsets alike."""
+    return _i8_product("sq_grouped_dgrad_w8", dy, p.n, p.k, p, offsets, out_dtype, workspace, out,
+                       "dy")
+
+
 # ---------------------------------------------------------------- MXFP4 mode
 @dataclass
 class MX4Payload:

@@ -101,7 +101,8 @@ const char* sq_status_str(sq_status_t s) {
     case SQ_OK: return "ok";
     case SQ_E_NULL: return "a required pointer is NULL";
     case SQ_E_SHAPE:
-      return "bad shape: need K % 256 == 0, K >= 256, N >= 1, M >= 0 (input gradient: N % 64 == 0)";
+      return "bad shape: need K % 256 == 0, K >= 256, N >= 1, M >= 0 (W4 input gradient: N % 64 == 0; "
+             "8-bit products: K <= 65536, M < 2^31, groups >= 1, input gradient N <= 131072)";
     case SQ_E_GROUP: return "group must be 32 or 64";
     case SQ_E_RANK: return "rank must be 0, 32 or 64 (int8 mode: 0, 16, 32 or 64; reserved 0)";
     case SQ_E_ALIGN: return "every pointer must be 16-byte aligned";
@@ -328,6 +329,101 @@ sq_status_t sq_linear_fwd_w8(const uint16_t* x, int64_t m, const sq_w8_t* p, voi
   return from_hip(sq::launch_fwd_contract(plan, reinterpret_cast<const uint8_t*>(p->codes),
                                           p->scales, p->lora_up, y, y_dtype == SQ_BF16, workspace,
                                           s));
+}
+
+// ---------------------------------------------------------------- 8-bit products
+// Sizes that the 8-bit products take: a row of x on one workgroup (K <= 65536),
+// exact int32 sums, 32-bit row numbers and a launch of fewer than 2^31 workgroups.
+constexpr int64_t kI8MaxK = 65536, kI8MaxN = 131072;
+
+static bool i8_shape_ok(int64_t m, int32_t groups, const sq_w8_t* p, bool dgrad) {
+  if (m < 0 || m > INT32_MAX || groups < 1 || p->k > kI8MaxK || p->n > INT32_MAX) return false;
+  if (dgrad && p->n > kI8MaxN) return false;
+  // offsets that are not ordered can name up to ceil(m / 16) tiles per group,
+  // which the device counts in 32 bits
+  if ((m + 15) / 16 > INT32_MAX / groups) return false;
+  const int64_t tiles = sq::i8_tile_bound(m, groups, 16);
+  return tiles <= INT32_MAX / ((p->n + 15) / 16) && tiles <= INT32_MAX / (p->k / 16);
+}
+
+static size_t i8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t* p, bool dgrad) {
+  if (!p || m <= 0 || p->k < 256 || p->k % 256 || p->n < 1) return 0;
+  if (p->rank != 0 && p->rank != 16 && p->rank != 32 && p->rank != 64) return 0;
+  if (!i8_shape_ok(m, groups, p, dgrad)) return 0;
+  return dgrad ? sq::plan_w8_dgrad(m, p->n, p->k, groups, p->rank).total
+               : sq::plan_w8a8(m, p->n, p->k, groups, p->rank).total;
+}
+
+// in is x [m][k] (forward) or dy [m][n] (input gradient); offsets is null for one layer
+static sq_status_t i8_product(const uint16_t* in, int64_t m, const int32_t* offsets, bool grouped,
+                              int32_t groups, const sq_w8_t* p, void* out, sq_dtype_t out_dtype,
+                              void* workspace, size_t workspace_bytes, void* stream, bool dgrad) {
+  if (out_dtype != SQ_F32 && out_dtype != SQ_BF16) return SQ_E_DTYPE;
+  sq_status_t st = check_payload_w8(p);
+  if (st != SQ_OK) return st;
+  if (!i8_shape_ok(m, groups, p, dgrad)) return SQ_E_SHAPE;
+  if (m == 0) return SQ_OK;
+  if (!in || !out || !workspace || (grouped && !offsets)) return SQ_E_NULL;
+  if (!aligned16(in) || !aligned16(out) || !aligned16(workspace) || !aligned16(offsets))
+    return SQ_E_ALIGN;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int bf16 = out_dtype == SQ_BF16;
+  if (dgrad) {
+    const sq::W8DgradPlan plan = sq::plan_w8_dgrad(m, p->n, p->k, groups, p->rank);
+    if (workspace_bytes < plan.total) return SQ_E_WORKSPACE;
+    if ((st = check_device()) != SQ_OK) return st;
+    return from_hip(sq::launch_w8_dgrad(plan, in, offsets, p->codes, p->scales, p->lora_up,
+                                        p->lora_down, out, bf16, workspace, s));
+  }
+  const sq::W8A8Plan plan = sq::plan_w8a8(m, p->n, p->k, groups, p->rank);
+  if (workspace_bytes < plan.total) return SQ_E_WORKSPACE;
+  if ((st = check_device()) != SQ_OK) return st;
+  return from_hip(sq::launch_w8a8(plan, in, offsets, p->codes, p->scales, p->lora_up,
+                                  p->lora_down, out, bf16, workspace, s));
+}
+
+size_t sq_linear_fwd_w8a8_workspace_bytes(int64_t m, const sq_w8_t* p) {
+  return i8_workspace_bytes(m, 1, p, false);
+}
+
+sq_status_t sq_linear_fwd_w8a8(const uint16_t* x, int64_t m, const sq_w8_t* p, void* y,
+                               sq_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  return i8_product(x, m, nullptr, false, 1, p, y, y_dtype, workspace, workspace_bytes, stream,
+                    false);
+}
+
+size_t sq_linear_dgrad_w8_workspace_bytes(int64_t m, const sq_w8_t* p) {
+  return i8_workspace_bytes(m, 1, p, true);
+}
+
+sq_status_t sq_linear_dgrad_w8(const uint16_t* dy, int64_t m, const sq_w8_t* p, void* dx,
+                               sq_dtype_t dx_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  return i8_product(dy, m, nullptr, false, 1, p, dx, dx_dtype, workspace, workspace_bytes, stream,
+                    true);
+}
+
+size_t sq_grouped_fwd_w8a8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t* p) {
+  return i8_workspace_bytes(m, groups, p, false);
+}
+
+sq_status_t sq_grouped_fwd_w8a8(const uint16_t* x, int64_t m, const int32_t* offsets,
+                                int32_t groups, const sq_w8_t* p, void* y, sq_dtype_t y_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return i8_product(x, m, offsets, true, groups, p, y, y_dtype, workspace, workspace_bytes, stream,
+                    false);
+}
+
+size_t sq_grouped_dgrad_w8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t* p) {
+  return i8_workspace_bytes(m, groups, p, true);
+}
+
+sq_status_t sq_grouped_dgrad_w8(const uint16_t* dy, int64_t m, const int32_t* offsets,
+                                int32_t groups, const sq_w8_t* p, void* dx, sq_dtype_t dx_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return i8_product(dy, m, offsets, true, groups, p, dx, dx_dtype, workspace, workspace_bytes,
+                    stream, true);
 }
 
 // ---------------------------------------------------------------- MXFP4 mode

@@ -1,0 +1,219 @@
+// Device helpers of the 8-bit products (forward and input gradient of the
+// int8 mode, for one layer and for experts): the map from workgroups to row
+// tiles of ragged groups, and the rank-r projection of the pre-phases.
+#pragma once
+#include "sq_device.hpp"
+
+namespace sq {
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* i8_lds_t;
+
+// Rows and scales are floored here so that 127 / absmax and 32512 / absmax stay finite.
+constexpr float I8_MIN_ABSMAX = 0x1p-100f;
+// Added to a float of magnitude below 2^22 it leaves round-to-nearest-even of
+// the value as an integer in the low mantissa bits (two's complement bytes).
+constexpr float I8_ROUND = 12582912.0f;   // 1.5 * 2^23
+constexpr uint32_t I8_NAN_BITS = 0x7FC00000u;
+
+// ---------------------------------------------------------------- row tiles
+// Rows offsets[e] .. offsets[e+1]-1 belong to group e.  The values come from
+// device memory, so no host check covers them: each range is clamped into
+// [0, m] here and every access derived from it stays inside the tensors.
+struct RowTile {
+  int group, rows;
+  int row0;
+};
+
+__device__ __forceinline__ void group_range(const int32_t* __restrict__ offsets, int groups, int m,
+                                            int e, int& lo, int& hi) {
+  lo = hi = 0;
+  if (e < groups) {
+    lo = min(max(offsets[e], 0), m);
+    hi = min(max(offsets[e + 1], lo), m);
+  }
+}
+
+// Number of tile_m-row tiles of all groups (offsets == null: one group of m rows).
+__device__ __forceinline__ int row_tile_count(const int32_t* __restrict__ offsets, int groups,
+                                              int m, int tile_m, int lane) {
+  if (!offsets) return (m + tile_m - 1) / tile_m;
+  int sum = 0;
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    int lo, hi;
+    group_range(offsets, groups, m, e0 + lane, lo, hi);
+    sum += (hi - lo + tile_m - 1) / tile_m;
+  }
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+
+// Tile t in group order; false past the last one.  All 64 lanes take part.
+__device__ __forceinline__ bool find_row_tile(const int32_t* __restrict__ offsets, int groups,
+                                              int m, int tile_m, int t, int lane, RowTile& out) {
+  if (!offsets) {
+    out.group = 0;
+    out.row0 = t * tile_m;
+    out.rows = min(tile_m, m - out.row0);
+    return out.rows > 0;
+  }
+  int base = 0;
+  for (int e0 = 0; e0 < groups; e0 += 64) {
+    int lo, hi;
+    group_range(offsets, groups, m, e0 + lane, lo, hi);
+    const int cnt = (hi - lo + tile_m - 1) / tile_m;
+    int inc = cnt;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int v = __shfl_up(inc, s);
+      if (lane >= s) inc += v;
+    }
+    const uint64_t past = __ballot(base + inc > t);
+    if (past) {
+      const int src = __builtin_ctzll(past);
+      const int first = base + __builtin_amdgcn_readlane(inc - cnt, src);
+      out.group = e0 + src;
+      out.row0 = __builtin_amdgcn_readlane(lo, src) + (t - first) * tile_m;
+      out.rows = min(tile_m, __builtin_amdgcn_readlane(hi, src) - out.row0);
+      return true;
+    }
+    base += __builtin_amdgcn_readlane(inc, 63);
+  }
+  return false;
+}
+
+// Group of a row (nondecreasing offsets); -1 for a row behind the last group.
+__device__ __forceinline__ int group_of_row(const int32_t* __restrict__ offsets, int groups,
+                                            int row, int lane) {
+  if (!offsets) return 0;
+  int e = 0;
+  for (int e0 = 0; e0 < groups; e0 += 64)
+    e += __popcll(__ballot(e0 + lane < groups && offsets[min(e0 + lane, groups - 1) + 1] <= row));
+  return e < groups ? e : -1;
+}
+
+// Eight consecutive 16-bit values from a 2-byte aligned address (one load:
+// the hardware takes unaligned vector loads); values at or past `left` read
+// as zero and are not touched in memory.
+__device__ __forceinline__ u32x4 load8_u16(const uint16_t* __restrict__ p, int left) {
+  u32x4 v = {0u, 0u, 0u, 0u};
+  if (left >= 8) {
+    __builtin_memcpy(&v, p, 16);
+  } else {
+    for (int i = 0; i < left; ++i) v[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+  }
+  return v;
+}
+
+// ---------------------------------------------------------------- rank-r projection
+// t_part[slice][row][r] = sum over the slice's columns of a[row][c] fac[c][r]
+// for the 16 rows of one tile: a bf16 [m][cols], fac bf16 [cols][rank] (the
+// group's factor), exact products and fp32 sums on bf16 MFMA.  The workgroup's
+// waves take the slice's 256-column blocks in turn and their sums are added
+// in wave order, so the result does not depend on timing.  Each wave stages
+// 32 factor rows in its own LDS (2 * 32 * rank bytes) and reads them
+// transposed (eight consecutive c of one rank column per lane).
+// mem: dynamic LDS, 64 * rank bytes per wave (also holds the partial sums).
+template <int RANK>
+__device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
+                                             const uint16_t* __restrict__ fac,
+                                             float* __restrict__ t_part, uint8_t* mem, int m,
+                                             int cols, const RowTile& rt, int slice, int slices) {
+  constexpr int RT = RANK / 16;
+  const int tid = threadIdx.x, lane = tid & 63, fr = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
+  const int blocks = (cols + 255) >> 8;
+  const int b0 = (int)((int64_t)slice * blocks / slices);
+  const int b1 = (int)((int64_t)(slice + 1) * blocks / slices);
+  uint8_t* stage = mem + wave * 64 * RANK;
+  const uint16_t* arow = a + (int64_t)(rt.row0 + min(fr, rt.rows - 1)) * cols;
+  f32x4 acc[RT] = {};
+  for (int b = b0 + wave; b < b1; b += waves) {
+#pragma unroll 2
+    for (int s = 0; s < 8; ++s) {
+      const int c0 = b * 256 + 32 * s;
+      if (c0 >= cols) break;
+      const u32x4 av = load8_u16(arow + c0 + 8 * g, cols - (c0 + 8 * g));
+      // 32 factor rows of RANK values: RANK / 16 chunks of 16 bytes per lane
+      u32x4 fv[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) {
+        const int q = 64 * j + lane;             // 16-byte chunk of the 32 rows
+        const int c = c0 + q / (RANK / 8);
+        fv[j] = (u32x4){0u, 0u, 0u, 0u};
+        if (c < cols)
+          fv[j] = *reinterpret_cast<const u32x4*>(fac + (int64_t)c * RANK + 8 * (q % (RANK / 8)));
+      }
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+        *reinterpret_cast<u32x4*>(stage + 16 * (64 * j + lane)) = fv[j];
+      __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
+      __builtin_amdgcn_wave_barrier();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+      for (int rt16 = 0; rt16 < RT; ++rt16) {
+        // transposed reads of four rows each: lane 4j + q of a 16-lane group
+        // points at row j, columns 4q..4q+3; lane i receives column i
+        s16x4 h[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int row = 8 * g + 4 * u + (fr >> 2), col = 16 * rt16 + 4 * (fr & 3);
+          h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(stage + 2 * (row * RANK + col)));
+        }
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const s16x8 bv = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+        acc[rt16] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
+                                                            __builtin_bit_cast(bf16x8, bv),
+                                                            acc[rt16], 0, 0, 0);
+      }
+      __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);   // the reads are done before the next write
+      __builtin_amdgcn_wave_barrier();
+      __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    }
+  }
+  // acc[r16][i]: row 4g + i, rank column 16 r16 + fr
+  float* red = reinterpret_cast<float*>(stage);
+#pragma unroll
+  for (int r16 = 0; r16 < RT; ++r16)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[(4 * g + i) * RANK + 16 * r16 + fr] = acc[r16][i];
+  __syncthreads();
+  for (int i = tid; i < rt.rows * RANK; i += blockDim.x) {
+    float t = 0.0f;
+    for (int w = 0; w < waves; ++w) t += reinterpret_cast<const float*>(mem + w * 64 * RANK)[i];
+    t_part[((int64_t)slice * m + rt.row0) * RANK + i] = t;
+  }
+}
+
+// t of one row, eight rank columns from r0, summed over the slices in order
+// and split into bf16 hi + lo MFMA operands.
+__device__ __forceinline__ void project_sum8(const float* __restrict__ t_part, int m, int rank,
+                                             int slices, int row, int r0, bf16x8& hi, bf16x8& lo) {
+  float t[8] = {};
+  for (int s = 0; s < slices; ++s) {
+    const float* p = t_part + ((int64_t)s * m + row) * rank + r0;
+    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[i] += a[i];
+      t[4 + i] += b[i];
+    }
+  }
+  u32x4 h, l;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t p = pack_bf16x2(t[2 * i], t[2 * i + 1]);
+    h[i] = p;
+    l[i] = pack_bf16x2(t[2 * i] - __uint_as_float(p << 16),
+                       t[2 * i + 1] - __uint_as_float(p & 0xFFFF0000u));
+  }
+  hi = __builtin_bit_cast(bf16x8, h);
+  lo = __builtin_bit_cast(bf16x8, l);
+}
+
+}  // namespace sq

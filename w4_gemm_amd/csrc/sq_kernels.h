@@ -107,4 +107,34 @@ hipError_t launch_dgrad(const DgradPlan& plan, const uint16_t* dy, const uint8_t
                         const uint16_t* scales, const uint16_t* up, const uint16_t* down,
                         void* dx, int dx_bf16, void* workspace, hipStream_t stream);
 
+// 8-bit products of the int8 mode.  offsets == null: one layer (groups = 1);
+// else rows offsets[e] .. offsets[e+1]-1 use expert e of stacked payloads.
+int64_t i8_tile_bound(int64_t m, int groups, int tile_m);
+int i8_project_slices(int64_t tiles16, int64_t cols, int waves);
+
+struct W8A8Plan {
+  int64_t m, n, k;
+  int groups, rank;
+  int prep_rows, prep_waves;   // rows and waves of a pre-phase workgroup
+  int slices;                  // K slices of the rank-r projection
+  size_t off_xq, off_xs, off_t, total;
+};
+W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank);
+hipError_t launch_w8a8(const W8A8Plan& plan, const uint16_t* x, const int32_t* offsets,
+                       const int8_t* codes, const uint16_t* scales, const uint16_t* up,
+                       const uint16_t* down, void* y, int y_bf16, void* workspace,
+                       hipStream_t stream);
+
+struct W8DgradPlan {
+  int64_t m, n, k, npad;       // npad: n rounded up to the 64-row stage
+  int groups, rank;
+  int slices;                  // N slices of the rank-r projection
+  size_t off_hi, off_lo, off_ts, off_t, total;
+};
+W8DgradPlan plan_w8_dgrad(int64_t m, int64_t n, int64_t k, int groups, int rank);
+hipError_t launch_w8_dgrad(const W8DgradPlan& plan, const uint16_t* dy, const int32_t* offsets,
+                           const int8_t* codes, const uint16_t* scales, const uint16_t* up,
+                           const uint16_t* down, void* dx, int dx_bf16, void* workspace,
+                           hipStream_t stream);
+
 }  // namespace sq

@@ -69,6 +69,27 @@ def check_w8_payload(codes, scales, up, down) -> tuple:
     return n, k, r
 
 
+def check_grouped_w8_payload(codes, scales, up, down) -> tuple:
+    """Stacked int8-residual payloads of E experts: codes i8 [E, N, K], scales fp16 [E, N],
+    up [E, N, r], down [E, K, r].  Returns (groups, n, k, rank)."""
+    codes = _shape(codes)
+    if len(codes) != 3 or codes[0] < 1:
+        raise ValueError("codes must be 3-D [E, N, K] with E >= 1")
+    e = codes[0]
+    _need("scales", scales, (e, codes[1]))
+    for name, f in (("lora_up", up), ("lora_down", down)):
+        if f is not None and (len(_shape(f)) != 3 or _shape(f)[0] != e):
+            raise ValueError(f"{name} must be 3-D [E, ., r] with E = {e}")
+    n, k, r = check_w8_payload(codes[1:], (codes[1],), None if up is None else _shape(up)[1:],
+                               None if down is None else _shape(down)[1:])
+    return e, n, k, r
+
+
+def check_offsets(offsets, groups: int) -> None:
+    """Row offsets of the experts: 1-D, one more than there are experts."""
+    _need("offsets", offsets, (groups + 1,))
+
+
 def check_mx4_payload(codes, exps, up, down) -> tuple:
     """MXFP4 payload: codes u8 [N, K/2], exps u8 [N, K/32], up [N, r], down [K, r]."""
     codes = _shape(codes)

@@ -232,43 +232,43 @@ def sq_linear_fwd_w8(x, m: int, p: SqW8, y, y_dtype: int, workspace, workspace_b
 
 
 def sq_linear_fwd_w8a8_workspace_bytes(m: int, p: SqW8) -> int:
-    return lib().sq_linear_fwd_w8a8_workspace_bytes(m, ctypes.byref(p))
+    return (_lib or lib()).sq_linear_fwd_w8a8_workspace_bytes(m, p)
 
 
 def sq_linear_fwd_w8a8(x, m: int, p: SqW8, y, y_dtype: int, workspace, workspace_bytes: int,
                        stream) -> int:
-    return lib().sq_linear_fwd_w8a8(x, m, ctypes.byref(p), y, y_dtype, workspace,
-                                    workspace_bytes, stream)
+    return (_lib or lib()).sq_linear_fwd_w8a8(x, m, p, y, y_dtype, workspace, workspace_bytes,
+                                              stream)
 
 
 def sq_linear_dgrad_w8_workspace_bytes(m: int, p: SqW8) -> int:
-    return lib().sq_linear_dgrad_w8_workspace_bytes(m, ctypes.byref(p))
+    return (_lib or lib()).sq_linear_dgrad_w8_workspace_bytes(m, p)
 
 
 def sq_linear_dgrad_w8(dy, m: int, p: SqW8, dx, dx_dtype: int, workspace, workspace_bytes: int,
                        stream) -> int:
-    return lib().sq_linear_dgrad_w8(dy, m, ctypes.byref(p), dx, dx_dtype, workspace,
-                                    workspace_bytes, stream)
+    return (_lib or lib()).sq_linear_dgrad_w8(dy, m, p, dx, dx_dtype, workspace, workspace_bytes,
+                                              stream)
 
 
 def sq_grouped_fwd_w8a8_workspace_bytes(m: int, groups: int, p: SqW8) -> int:
-    return lib().sq_grouped_fwd_w8a8_workspace_bytes(m, groups, ctypes.byref(p))
+    return (_lib or lib()).sq_grouped_fwd_w8a8_workspace_bytes(m, groups, p)
 
 
 def sq_grouped_fwd_w8a8(x, m: int, offsets, groups: int, p: SqW8, y, y_dtype: int, workspace,
                         workspace_bytes: int, stream) -> int:
-    return lib().sq_grouped_fwd_w8a8(x, m, offsets, groups, ctypes.byref(p), y, y_dtype,
-                                     workspace, workspace_bytes, stream)
+    return (_lib or lib()).sq_grouped_fwd_w8a8(x, m, offsets, groups, p, y, y_dtype, workspace,
+                                               workspace_bytes, stream)
 
 
 def sq_grouped_dgrad_w8_workspace_bytes(m: int, groups: int, p: SqW8) -> int:
-    return lib().sq_grouped_dgrad_w8_workspace_bytes(m, groups, ctypes.byref(p))
+    return (_lib or lib()).sq_grouped_dgrad_w8_workspace_bytes(m, groups, p)
 
 
 def sq_grouped_dgrad_w8(dy, m: int, offsets, groups: int, p: SqW8, dx, dx_dtype: int, workspace,
                         workspace_bytes: int, stream) -> int:
-    return lib().sq_grouped_dgrad_w8(dy, m, offsets, groups, ctypes.byref(p), dx, dx_dtype,
-                                     workspace, workspace_bytes, stream)
+    return (_lib or lib()).sq_grouped_dgrad_w8(dy, m, offsets, groups, p, dx, dx_dtype,
+                                               workspace, workspace_bytes, stream)
 
 
 def sq_quantize_weight_mx4(w, p: SqMx4, dev_flags, stream) -> int:

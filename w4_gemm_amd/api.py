@@ -50,6 +50,8 @@ class W4Payload:
 
 def _require(t, dtype, name):
     """The C ABI takes dense row-major device buffers: refuse anything else."""
+    if t.dtype is dtype and t.is_cuda and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if not t.is_cuda:
@@ -74,6 +76,11 @@ def _nbytes(t):
 
 def _stream():
     return torch.cuda.current_stream().cuda_stream
+
+
+def _raw_stream(device: int):
+    """_stream() without the Stream object around it (a tenth of the time)."""
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _check(status: int, where: str):
@@ -342,43 +349,54 @@ def stack_payloads_w8(payloads) -> GroupedW8Payload:
         torch.stack([p.down for p in payloads]) if first.rank else None)
 
 
-def _on_current_device(*tensors):
-    """Refuse tensors of another device than the one the kernels would run on."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != cur:
-            raise ValueError(f"tensors must live on the current device (cuda:{cur}), "
-                             f"got {t.device}")
+def _dense(t, dtype, name, device):
+    """_require, and on the device that the kernels run on (one pass over the usual case: the
+    smallest products take as long as their checks)."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous():
+        _require(t, dtype, name)
+    if t.get_device() != device:
+        raise ValueError(f"tensors must live on the current device (cuda:{device}), {name} is on "
+                         f"{t.device}")
 
 
-def _i8_product(name, a, cols_in, cols_out, p, offsets, out_dtype, workspace, out, in_name):
-    """The common part of the four 8-bit products (checks, allocation, call)."""
-    _require(a, torch.bfloat16, in_name)
+_OUT_DTYPES = {torch.float32: SQ_F32, torch.bfloat16: SQ_BF16}
+
+
+def _i8_product(call, sizes, a, into, p, offsets, out_dtype, workspace, out, in_name):
+    """The common part of the four 8-bit products (checks, allocation, call).  `into` is the
+    payload's (columns of a, columns of the result)."""
+    dev = torch.cuda.current_device()
+    _dense(a, torch.bfloat16, in_name, dev)
+    cols_in, cols_out = into
     m = S.check_rows(in_name, a.shape, cols_in)
     abi = p.abi()
+    for t in (p.codes, p.scales, p.up, p.down):
+        if t is not None and t.get_device() != dev:
+            _dense(t, t.dtype, "the payload", dev)
+    groups = ()
+    if offsets is not None:
+        _dense(offsets, torch.int32, "offsets", dev)
+        S.check_offsets(offsets.shape, p.groups)
+        groups = (offsets.data_ptr(), p.groups)
     if out is None:
-        if out_dtype not in (torch.float32, torch.bfloat16):
+        if out_dtype not in _OUT_DTYPES:
             raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
         out = torch.empty((m, cols_out), dtype=out_dtype, device=a.device)
-    _require(out, out.dtype, "out")
-    if out.dtype not in (torch.float32, torch.bfloat16):
-        raise ValueError("out must be fp32 or bf16")
-    S.check_out("out", out.shape, (m, cols_out))
-    dt = SQ_BF16 if out.dtype == torch.bfloat16 else SQ_F32
-    if offsets is None:
-        nbytes = getattr(_lib, name + "_workspace_bytes")(m, abi)
     else:
-        _require(offsets, torch.int32, "offsets")
-        S.check_offsets(offsets.shape, p.groups)
-        nbytes = getattr(_lib, name + "_workspace_bytes")(m, p.groups, abi)
+        _dense(out, out.dtype, "out", dev)
+        S.check_out("out", out.shape, (m, cols_out))
+        if out.dtype not in _OUT_DTYPES:
+            raise ValueError("out must be fp32 or bf16")
     if workspace is None:
+        nbytes = sizes(m, *groups[1:], abi)
         workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=a.device)
-    _on_current_device(a, p.codes, p.scales, p.up, p.down, offsets, out, workspace)
-    tail = (abi, out.data_ptr(), dt, workspace.data_ptr(), _nbytes(workspace), _stream())
-    if offsets is None:
-        _check(getattr(_lib, name)(a.data_ptr(), m, *tail), name)
     else:
-        _check(getattr(_lib, name)(a.data_ptr(), m, offsets.data_ptr(), p.groups, *tail), name)
+        _dense(workspace, workspace.dtype, "workspace", dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    status = call(a.data_ptr(), m, *groups, abi, out.data_ptr(), _OUT_DTYPES[out.dtype],
+                  workspace.data_ptr(), nbytes, _raw_stream(dev))
+    if status != _lib.SQ_OK:
+        raise SqError(status, call.__name__)
     return out
 
 
@@ -389,7 +407,8 @@ def fwd_w8a8_workspace_bytes(m: int, p: W8Payload) -> int:
 def linear_fwd_w8a8(x: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """sq_linear_fwd_w8a8: bf16 x [M,K] -> y [M,N] (fp32 or bf16), 8-bit tokens and weights."""
-    return _i8_product("sq_linear_fwd_w8a8", x, p.k, p.n, p, None, out_dtype, workspace, out, "x")
+    return _i8_product(_lib.sq_linear_fwd_w8a8, _lib.sq_linear_fwd_w8a8_workspace_bytes, x,
+                       (p.k, p.n), p, None, out_dtype, workspace, out, "x")
 
 
 def dgrad_w8_workspace_bytes(m: int, p: W8Payload) -> int:
@@ -399,8 +418,8 @@ def dgrad_w8_workspace_bytes(m: int, p: W8Payload) -> int:
 def linear_dgrad_w8(dy: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """sq_linear_dgrad_w8: bf16 dy [M,N] -> dx = dy @ W_hat [M,K] (fp32 or bf16)."""
-    return _i8_product("sq_linear_dgrad_w8", dy, p.n, p.k, p, None, out_dtype, workspace, out,
-                       "dy")
+    return _i8_product(_lib.sq_linear_dgrad_w8, _lib.sq_linear_dgrad_w8_workspace_bytes, dy,
+                       (p.n, p.k), p, None, out_dtype, workspace, out, "dy")
 
 
 def grouped_fwd_w8a8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
@@ -414,8 +433,8 @@ def grouped_fwd_w8a8(x: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payload
 
     offsets is an int32 device tensor [E+1]; rows outside the experts' ranges are left as they
     were in `out` (undefined when it is allocated here)."""
-    return _i8_product("sq_grouped_fwd_w8a8", x, p.k, p.n, p, offsets, out_dtype, workspace, out,
-                       "x")
+    return _i8_product(_lib.sq_grouped_fwd_w8a8, _lib.sq_grouped_fwd_w8a8_workspace_bytes, x,
+                       (p.k, p.n), p, offsets, out_dtype, workspace, out, "x")
 
 
 def grouped_dgrad_w8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
@@ -426,8 +445,8 @@ def grouped_dgrad_w8(dy: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payloa
                      out_dtype=torch.float32, workspace: torch.Tensor | None = None,
                      out: torch.Tensor | None = None):
     """sq_grouped_dgrad_w8: the input gradient of grouped_fwd_w8a8, rows and offsets alike."""
-    return _i8_product("sq_grouped_dgrad_w8", dy, p.n, p.k, p, offsets, out_dtype, workspace, out,
-                       "dy")
+    return _i8_product(_lib.sq_grouped_dgrad_w8, _lib.sq_grouped_dgrad_w8_workspace_bytes, dy,
+                       (p.n, p.k), p, offsets, out_dtype, workspace, out, "dy")
 
 
 # ---------------------------------------------------------------- MXFP4 mode

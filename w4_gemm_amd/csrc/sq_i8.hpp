@@ -191,29 +191,35 @@ __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
 }
 
 // t of one row, eight rank columns from r0, summed over the slices in order
-// and split into bf16 hi + lo MFMA operands.
+// and split into three bf16 parts: hi + lo hold t to 2^-16, the third to 2^-24.
 __device__ __forceinline__ void project_sum8(const float* __restrict__ t_part, int m, int rank,
-                                             int slices, int row, int r0, bf16x8& hi, bf16x8& lo) {
+                                             int slices, int row, int r0, u32x4 (&part)[3]) {
   float t[8] = {};
-  for (int s = 0; s < slices; ++s) {
-    const float* p = t_part + ((int64_t)s * m + row) * rank + r0;
-    const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+  const float* p = t_part + (int64_t)row * rank + r0;
+  const int64_t step = (int64_t)m * rank;
+  // four slices' loads in flight; a slice past the last one adds zero
+  for (int s = 0; s < slices; s += 4) {
+    f32x4 v[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const f32x4* q = reinterpret_cast<const f32x4*>(p + min(s + u, slices - 1) * step);
+      v[u][0] = q[0];
+      v[u][1] = q[1];
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] += s + u < slices ? v[u][i >> 2][i & 3] : 0.0f;
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      t[i] += a[i];
-      t[4 + i] += b[i];
+      const uint32_t p = pack_bf16x2(t[2 * i], t[2 * i + 1]);
+      part[q][i] = p;
+      t[2 * i] -= __uint_as_float(p << 16);
+      t[2 * i + 1] -= __uint_as_float(p & 0xFFFF0000u);
     }
-  }
-  u32x4 h, l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t p = pack_bf16x2(t[2 * i], t[2 * i + 1]);
-    h[i] = p;
-    l[i] = pack_bf16x2(t[2 * i] - __uint_as_float(p << 16),
-                       t[2 * i + 1] - __uint_as_float(p & 0xFFFF0000u));
-  }
-  hi = __builtin_bit_cast(bf16x8, h);
-  lo = __builtin_bit_cast(bf16x8, l);
 }
 
 }  // namespace sq

@@ -116,8 +116,11 @@ struct W8A8Plan {
   int64_t m, n, k;
   int groups, rank;
   int prep_rows, prep_waves;   // rows and waves of a pre-phase workgroup
+  int tile_m, tile_n;          // contraction tile
+  int waves;                   // small tiles: waves that split K
   int slices;                  // K slices of the rank-r projection
-  size_t off_xq, off_xs, off_t, total;
+  int splits;                  // K splits of the contraction
+  size_t off_xq, off_xs, off_t, off_part, total;
 };
 W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank);
 hipError_t launch_w8a8(const W8A8Plan& plan, const uint16_t* x, const int32_t* offsets,

@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
   // (q, p) is column 64 q + 16 g' + 4 p + i, MFMA column fr the lane's row
   for (int rr = 0; rr < rank; rr += 32) {
     const bool rk = rr + 8 * g < rank;
-    bf16x8 hi = {}, lo = {};
-    if (rk) project_sum8(t_part, m, rank, slices, rrow, rr + 8 * g, hi, lo);
+    u32x4 part[3] = {};
+    if (rk) project_sum8(t_part, m, rank, slices, rrow, rr + 8 * g, part);
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -333,8 +333,10 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
                              : (bf16x8){};
         const int b = 16 * q + 4 * p;
         f32x4 acc = {w[b], w[b + 1], w[b + 2], w[b + 3]};
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, hi, acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, lo, acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[0]), acc, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[1]), acc, 0, 0, 0);
+        if (!dx_bf16)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[2]), acc, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[b + i] = acc[i];
       }

@@ -21,6 +21,7 @@
 //   k_w8a8_gemm  q c^T on v_mfma_i32_16x16x64_i8 (exact: K <= 65536 keeps the
 //                sums below 2^31), scales and rank-r branch in the epilogue
 #include <algorithm>
+#include <cmath>
 
 #include "sq_i8.hpp"
 #include "sq_kernels.h"
@@ -160,39 +161,82 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 }
 
 // ---------------------------------------------------------------- contraction
-// 256 x 256 output tile per workgroup, eight waves of 128 x 64 (8 x 4 MFMA
-// tiles).  One stage = 64 bytes of K of each operand row; both operands
-// stream global -> LDS with direct 16-byte buffer loads into three stage
-// buffers, two stages ahead of the MFMAs.  Chunk c of row r sits at slot
-// c ^ ((r >> 1) & 3), which keeps the 16-byte fragment reads free of bank
-// conflicts.
-constexpr int G_BM = 256, G_BN = 256, G_THREADS = 512;
-constexpr int G_STAGE = 256 * 64;
+// BM x 256 output tile per workgroup (BM = 32 FM), eight waves of 16 FM x 64
+// (FM x 4 MFMA tiles).  One stage = 128 bytes of K of each operand row, two
+// stages in LDS.  Both operands stream global -> LDS with direct 16-byte
+// buffer loads that cover whole 128-byte lines (64-byte halves of lines cost
+// 5 % of the 4480 x 16384 x 6144 contraction).  Chunk c of LDS row r sits at
+// slot c ^ g_swz(r).
+// LDS row 64 w + 16 j + f of the weight holds output column 64 w + 4 f + j, so
+// that a lane ends up with four consecutive columns and stores them as they
+// are.
+constexpr int G_BN = 256, G_THREADS = 512;
+constexpr int G_STAGE = 256 * 128;
 __shared__ __attribute__((aligned(16))) uint8_t g_a0[G_STAGE];
 __shared__ __attribute__((aligned(16))) uint8_t g_a1[G_STAGE];
-__shared__ __attribute__((aligned(16))) uint8_t g_a2[G_STAGE];
 __shared__ __attribute__((aligned(16))) uint8_t g_b0[G_STAGE];
 __shared__ __attribute__((aligned(16))) uint8_t g_b1[G_STAGE];
-__shared__ __attribute__((aligned(16))) uint8_t g_b2[G_STAGE];
+__shared__ __attribute__((aligned(16))) float g_xs[256];
+__shared__ __attribute__((aligned(16))) float g_ws[256];
 
+// Swizzle of 128-byte rows.  A loop of nothing but the fragment reads runs
+// 1.9 times as long under c ^ (r & 7) ^ ((r >> 3) & 1), 3.7 times without any.
+__device__ __forceinline__ int g_swz(int r) { return r & 7; }
+
+// t of the tile's rows as bf16 parts (hi, lo and, for fp32 results, a third:
+// 2^-24 of t then) in LDS: part p, eight ranks r8, row -> 16 bytes.
+template <int BM>
+__device__ __forceinline__ uint8_t* t_chunk(int part, int r8, int row, int rank8) {
+  const int at = ((part * rank8 + r8) * BM + row) * 16;
+  // at most 3 * 8 * 256 chunks; the stage buffers are separate objects
+  uint8_t* base = at < G_STAGE ? g_a0 : at < 2 * G_STAGE ? g_a1 : g_b0;
+  return base + (at & (G_STAGE - 1));
+}
+
+// Four consecutive values of a row, fp32 or bf16; `left` columns remain (rows
+// of an odd N are 4- or 2-byte aligned only).
+__device__ __forceinline__ void store4(void* __restrict__ y, int64_t at, f32x4 o, int left,
+                                       int y_bf16) {
+  if (y_bf16) {
+    uint16_t* dst = reinterpret_cast<uint16_t*>(y) + at;
+    const u32x2 b = {pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+    if (left >= 4) {
+      __builtin_memcpy(dst, &b, 8);
+    } else {
+      for (int c = 0; c < left; ++c) dst[c] = (uint16_t)(b[c >> 1] >> (16 * (c & 1)));
+    }
+  } else {
+    float* dst = reinterpret_cast<float*>(y) + at;
+    if (left >= 4) {
+      __builtin_memcpy(dst, &o, 16);
+    } else {
+      for (int c = 0; c < left; ++c) dst[c] = o[c];
+    }
+  }
+}
+
+template <int FM, bool SPLIT>
 __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     const int8_t* __restrict__ xq, const float* __restrict__ xs,
     const float* __restrict__ t_part, const int8_t* __restrict__ codes,
     const uint16_t* __restrict__ scales, const uint16_t* __restrict__ up,
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ y, int m, int n, int k,
-    int rank, int slices, int y_bf16) {
-  constexpr int FM = 8, FN = 4;
+    int rank, int slices, int y_bf16, int splits, int32_t* __restrict__ partial) {
+  constexpr int FN = 4, BM = 32 * FM;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int fr = lane & 15, g = lane >> 4;
   const int nt = (n + G_BN - 1) / G_BN;
-  const int mt = row_tile_count(offsets, groups, m, G_BM, lane);
-  if ((int64_t)blockIdx.x >= (int64_t)mt * nt) return;
+  const int mt = row_tile_count(offsets, groups, m, BM, lane);
+  // workgroup b: K split b / tiles of tile b % tiles
+  const int tiles = mt * nt;
+  const int split = __builtin_amdgcn_readfirstlane(tiles ? (int)blockIdx.x / tiles : splits);
+  if (split >= splits) return;
   int64_t tm, tn;
-  xcd_tile(blockIdx.x, (int64_t)mt * nt, nt, tm, tn);
+  xcd_tile((int)blockIdx.x - split * tiles, tiles, nt, tm, tn);
   RowTile rt;
-  if (!find_row_tile(offsets, groups, m, G_BM, __builtin_amdgcn_readfirstlane((int)tm), lane, rt))
+  if (!find_row_tile(offsets, groups, m, BM, __builtin_amdgcn_readfirstlane((int)tm), lane, rt))
     return;
   // scalar registers for everything the descriptors are built from
   const int grp = __builtin_amdgcn_readfirstlane(rt.group);
@@ -201,187 +245,496 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   const int n0 = __builtin_amdgcn_readfirstlane((int)tn) * G_BN;
   const int cols = min(G_BN, n - n0);
   const int64_t brow0 = (int64_t)grp * n + n0;   // first weight row of the tile
-  const int KT = k >> 6;
+  // stages of 128 values: an even number (the splits cut K in multiples of 256)
+  const int st0 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)split * (k >> 8) / splits));
+  const int ST =
+      2 * __builtin_amdgcn_readfirstlane((int)((int64_t)(split + 1) * (k >> 8) / splits)) - st0;
 
-  const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(xq + m0 * k), (short)0, rows * k, 0x00020000);
-  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-      (void*)(codes + brow0 * k), (short)0, cols * k, 0x00020000);
-  uint32_t off_a[2], off_b[2];
+  // loaders: instruction i of wave w fills LDS rows 64 i + 8 w .. +8, through a
+  // descriptor of its own (64 rows each) so that one offset serves all; rows
+  // past the tile lie beyond their descriptor and fetch nothing
+  constexpr int NA = (BM + 63) / 64;
+  const int lr = 8 * wave + (lane >> 3);
+  const uint32_t lslot = 16u * (uint32_t)((lane & 7) ^ g_swz(lr));
+  const uint32_t off_a = (uint32_t)lr * (uint32_t)k + lslot;
+  const uint32_t off_b = (uint32_t)(4 * (lr & 15) + (lr >> 4)) * (uint32_t)k + lslot;
+  const int8_t *a_base = xq + m0 * k, *b_base = codes + brow0 * k;
+  const int kb = st0 * 128;
+  auto issue = [&](int st, uint8_t* ab, uint8_t* bb) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int r = 32 * wave + 16 * i + (lane >> 2);
-    const uint32_t slot = (uint32_t)((lane & 3) ^ ((r >> 1) & 3));
-    off_a[i] = (uint32_t)min(r, rows - 1) * (uint32_t)k + 16u * slot;
-    off_b[i] = (uint32_t)min(r, cols - 1) * (uint32_t)k + 16u * slot;
-  }
-  auto issue = [&](int kt, uint8_t* ab, uint8_t* bb) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (i8_lds_t)(ab + (32 * wave + 16 * i) * 64),
-                                               16, off_a[i], kt * 64, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rsrc, (i8_lds_t)(bb + (32 * wave + 16 * i) * 64),
-                                               16, off_b[i], kt * 64, 0, 0);
+    for (int i = 0; i < 4; ++i) {
+      const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(a_base + (int64_t)(64 * i) * k), (short)0, max(rows - 64 * i, 0) * k, 0x00020000);
+      const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(b_base + (int64_t)(64 * i) * k), (short)0, max(cols - 64 * i, 0) * k, 0x00020000);
+      if (i < NA)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (i8_lds_t)(ab + (8 * i + wave) * 1024), 16,
+                                                 off_a, kb + st * 128, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16,
+                                               off_b, kb + st * 128, 0, 0);
     }
   };
-  const uint32_t swz = (uint32_t)(g ^ ((fr >> 1) & 3));
-  const uint32_t a_lane = (uint32_t)(128 * wm + fr) * 64 + 16 * swz;
-  const uint32_t b_lane = (uint32_t)(64 * wn + fr) * 64 + 16 * swz;
+  issue(0, g_a0, g_b0);
+  issue(min(1, ST - 1), g_a1, g_b1);
+  // scales of the tile's rows and columns, for the epilogue
+  if (tid < 256)
+    g_xs[tid] = xs[m0 + min(tid, rows - 1)];
+  else
+    g_ws[tid - 256] = fp16_bits_to_f32(scales[brow0 + min(tid - 256, cols - 1)]);
+
+  // fragment addresses: K half h is chunks 4 h .. 4 h + 3
+  const uint32_t a_row = (uint32_t)(16 * FM * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
+  uint32_t slot[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) slot[h] = 16u * (uint32_t)((4 * h + g) ^ g_swz(fr));
   i32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
-  auto compute = [&](const uint8_t* ab, const uint8_t* bb) {
-    i32x4 bf[FN];
+  struct Frag {
+    i32x4 a[FM], b[FN];
+  };
+  auto read = [&](Frag& f, const uint8_t* ab, const uint8_t* bb, int h) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) bf[j] = *reinterpret_cast<const i32x4*>(bb + b_lane + j * 1024);
+    for (int j = 0; j < FN; ++j)
+      f.b[j] = *reinterpret_cast<const i32x4*>(bb + b_row + slot[h] + j * 2048);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const i32x4 af = *reinterpret_cast<const i32x4*>(ab + a_lane + i * 1024);
+    for (int i = 0; i < FM; ++i)
+      f.a[i] = *reinterpret_cast<const i32x4*>(ab + a_row + slot[h] + i * 2048);
+  };
+  auto compute = [&](const Frag& f) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(af, bf[j], acc[i][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+  };
+  auto interleave = [&]() {
+#pragma unroll
+    for (int i = 0; i < FM + FN; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
+      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 4 ? 2 : 1, 0);   // two MFMAs
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, FM >= 4 ? FM * FN - 2 * (FM + FN) : 1, 0);
+  };
+  auto interleave_loads = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // one global load
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 2 ? FM * FN / 8 : 1, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 2 ? FM * FN / 8 : 1, 0);
     }
   };
   auto sync = [&]() {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(sq_wait_vm(4));
+    __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);
     __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage s lives in buffer s % 3.  Each step waits for its own loads of the
-  // stage (four of the next stage may still be in flight), meets the other
-  // waves, refills the buffer of stage s - 1 with stage s + 2 and computes.
-  // Loads past the last stage fetch the last one again, into a buffer that is
-  // not read any more.
-  issue(0, g_a0, g_b0);
-  issue(min(1, KT - 1), g_a1, g_b1);
-  int kt = 0;
-  for (; kt + 3 <= KT; kt += 3) {
+  // One stage.  The K half in registers is contracted while the next one is
+  // read.  At the barrier every wave has read all of the stage, so its buffers
+  // take stage st + 2, and stage st + 1 has landed.  Loads past the last stage
+  // fetch the last one again, into buffers that are not read any more.
+  Frag f0, f1;
+  auto stage = [&](int st, uint8_t* ab, uint8_t* bb, const uint8_t* an, const uint8_t* bn) {
+    read(f1, ab, bb, 1);
+    compute(f0);
+    interleave();
     sync();
-    issue(min(kt + 2, KT - 1), g_a2, g_b2);
-    compute(g_a0, g_b0);
-    sync();
-    issue(min(kt + 3, KT - 1), g_a0, g_b0);
-    compute(g_a1, g_b1);
-    sync();
-    issue(min(kt + 4, KT - 1), g_a1, g_b1);
-    compute(g_a2, g_b2);
-  }
-  if (kt < KT) {
-    sync();
-    issue(min(kt + 2, KT - 1), g_a2, g_b2);
-    compute(g_a0, g_b0);
-    if (kt + 1 < KT) {
-      sync();
-      compute(g_a1, g_b1);
-    }
+    issue(min(st + 2, ST - 1), ab, bb);
+    read(f0, an, bn, 0);
+    compute(f1);
+    interleave_loads();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  sync();
+  read(f0, g_a0, g_b0, 0);
+  for (int st = 0; st < ST; st += 2) {
+    stage(st, g_a0, g_b0, g_a1, g_b1);
+    stage(st + 1, g_a1, g_b1, g_a0, g_b0);
   }
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
-
-  // scales, the column's first: |acc w| < 2^47 cannot overflow whatever the
-  // row's magnitude is; acc[i][j][v] is row 128 wm + 16 i + 4 g + v, column 64 wn + 16 j + fr
-  const int rbase = 128 * wm, cbase = 64 * wn;
-  f32x4 out[FM][FN];
-  float wsc[FN];
   __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int j = 0; j < FN; ++j)
-    wsc[j] = fp16_bits_to_f32(scales[brow0 + min(cbase + 16 * j + fr, cols - 1)]);
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const float sr = xs[m0 + min(rbase + 16 * i + 4 * g + v, rows - 1)];
-#pragma unroll
-      for (int j = 0; j < FN; ++j) out[i][j][v] = (float)acc[i][j][v] * wsc[j] * sr;
-    }
-  // rank-r branch: (t_hi + t_lo) up^T (rank 16: the upper half of the 32-wide
-  // step reads zeros)
-  for (int rr = 0; rr < rank; rr += 32) {
-    const bool rk = rr + 8 * g < rank;
-    bf16x8 bu[FN];
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-      bu[j] = rk ? *reinterpret_cast<const bf16x8*>(
-                       up + (brow0 + min(cbase + 16 * j + fr, cols - 1)) * rank + rr + 8 * g)
-                 : (bf16x8){};
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      bf16x8 hi = {}, lo = {};
-      if (rk)
-        project_sum8(t_part, m, rank, slices, (int)m0 + min(rbase + 16 * i + fr, rows - 1),
-                     rr + 8 * g, hi, lo);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi, bu[j], out[i][j], 0, 0, 0);
-        out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo, bu[j], out[i][j], 0, 0, 0);
-      }
-    }
-  }
-  if (!y_bf16) {
-    float* yf = reinterpret_cast<float*>(y);
+
+  // acc[i][j][v] is row 16 (FM wm + i) + 4 g + v, column 64 wn + 4 fr + j
+  const int rbase = 16 * FM * wm, c0 = 64 * wn + 4 * fr, left = cols - c0;
+  if constexpr (SPLIT) {
+    // the splits' integer sums meet in k_w8a8_join
+    int32_t* dst = partial + ((int64_t)split * m + m0) * n + n0 + c0;
 #pragma unroll
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = rbase + 16 * i + 4 * g + v;
         if (r >= rows) continue;
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int c = cbase + 16 * j + fr;
-          if (c < cols) yf[(m0 + r) * n + n0 + c] = out[i][j][v];
+        const i32x4 o = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
+        if (left >= 4) {
+          __builtin_memcpy(dst + (int64_t)r * n, &o, 16);
+        } else {
+          for (int c = 0; c < left; ++c) dst[(int64_t)r * n + c] = o[c];
         }
       }
     return;
   }
-  // bf16: each wave turns 64 x 64 values at a time into 128-byte row segments
-  // in 8 KB of the stage buffers (16-byte chunk c of row r at slot
-  // c ^ a_swz(r)), so that every store instruction writes whole segments
-  __syncthreads();   // every wave is done with the stage buffers
-  const int wb = wave >> 1;
-  uint8_t* st = (wb == 0 ? g_a0 : wb == 1 ? g_a1 : wb == 2 ? g_b0 : g_b1) + (wave & 1) * 8192;
-  const bool wide = (n & 7) == 0;
+  const int rank8 = rank >> 3, parts = y_bf16 ? 2 : 3;
+  if (rank > 0) {
+    __syncthreads();   // every wave is done with the stage buffers
+    for (int q = tid; q < BM * rank8; q += G_THREADS) {
+      const int row = q % BM, r8 = q / BM;
+      u32x4 part[3];
+      project_sum8(t_part, m, rank, slices, (int)m0 + min(row, rows - 1), 8 * r8, part);
 #pragma unroll
-  for (int h = 0; h < FM / 4; ++h) {
+      for (int p = 0; p < 3; ++p)
+        if (p < parts) *reinterpret_cast<u32x4*>(t_chunk<BM>(p, r8, row, rank8)) = part[p];
+    }
+  }
+  // scales, the column's first: |acc w| < 2^47 cannot overflow whatever the
+  // row's magnitude is
+  f32x4 out[FM][FN];
+  const f32x4 wsc = *reinterpret_cast<const f32x4*>(&g_ws[c0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < FM; ++i) {
+    const f32x4 sr = *reinterpret_cast<const f32x4*>(&g_xs[rbase + 16 * i + 4 * g]);
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int lr = 16 * i + 4 * g + v;
+    for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          const int c = 16 * j + fr;
-          *reinterpret_cast<uint16_t*>(st + lr * 128 + 16 * ((c >> 3) ^ a_swz(lr)) + 2 * (c & 7)) =
-              f32_to_bf16(out[4 * h + i][j][v]);
+      for (int v = 0; v < 4; ++v) out[i][j][v] = (float)acc[i][j][v] * wsc[j] * sr[v];
+  }
+  // rank-r branch t up^T (rank 16: the upper half of the 32-wide step reads zeros)
+  if (rank > 0) {
+    __syncthreads();
+    for (int rr = 0; rr < rank8; rr += 4) {
+      const bool rk = rr + g < rank8;
+      bf16x8 bu[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        bu[j] = rk ? *reinterpret_cast<const bf16x8*>(
+                         up + (brow0 + min(c0 + j, cols - 1)) * rank + 8 * (rr + g))
+                   : (bf16x8){};
+      for (int p = 0; p < parts; ++p) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i) {
+          const bf16x8 at = rk ? *reinterpret_cast<const bf16x8*>(
+                                     t_chunk<BM>(p, rr + g, rbase + 16 * i + fr, rank8))
+                               : (bf16x8){};
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+            out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at, bu[j], out[i][j], 0, 0, 0);
         }
       }
-    __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
-    __builtin_amdgcn_wave_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    }
+  }
+  // stores of four columns: 16 lanes write one row's 128 (bf16) or 256 bytes
 #pragma unroll
-    for (int it = 0; it < 8; ++it) {
-      const int lr = 8 * it + (lane >> 3), chunk = lane & 7;
-      const int r = rbase + 64 * h + lr, c = cbase + 8 * chunk;
-      const u32x4 o = *reinterpret_cast<const u32x4*>(st + lr * 128 + 16 * (chunk ^ a_swz(lr)));
-      if (r >= rows || c >= cols) continue;
-      uint16_t* dst = reinterpret_cast<uint16_t*>(y) + (m0 + r) * n + n0 + c;
-      if (wide) {
-        *reinterpret_cast<u32x4*>(dst) = o;
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = rbase + 16 * i + 4 * g + v;
+      if (r >= rows) continue;
+      const f32x4 o = {out[i][0][v], out[i][1][v], out[i][2][v], out[i][3][v]};
+      store4(y, (m0 + r) * n + n0 + c0, o, left, y_bf16);
+    }
+}
+
+// Sum of the splits' integers (exact, in any order), scales and rank-r branch.
+// One workgroup takes 16 rows of one group x 64 columns, a thread four columns
+// of one row: at a few rows the partial sums are read by many workgroups with
+// up to eight loads of a thread in flight (a form of 16 rows x 256 columns with
+// the branch on MFMA took 7.8 us at 48 x 6144 and 8 splits).
+__global__ void __launch_bounds__(256) k_w8a8_join(
+    const int32_t* __restrict__ partial, const float* __restrict__ xs,
+    const float* __restrict__ t_part, const uint16_t* __restrict__ scales,
+    const uint16_t* __restrict__ up, const int32_t* __restrict__ offsets, int groups,
+    void* __restrict__ y, int m, int n, int rank, int slices, int y_bf16, int splits) {
+  __shared__ __attribute__((aligned(16))) float t_lds[16 * 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int nt = (n + 63) >> 6;
+  const int tile = (int)blockIdx.x / nt;
+  RowTile rt;
+  if (!find_row_tile(offsets, groups, m, 16, tile, lane, rt)) return;
+  const int lrow = tid >> 4, c0 = ((int)blockIdx.x - tile * nt) * 64 + 4 * (tid & 15);
+  const int left = n - c0, row = rt.row0 + min(lrow, rt.rows - 1);
+  i32x4 s = {0, 0, 0, 0};
+  for (int sp = 0; sp < splits; sp += 8) {
+    i32x4 p[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int32_t* src = partial + ((int64_t)min(sp + u, splits - 1) * m + row) * n + c0;
+      p[u] = (i32x4){0, 0, 0, 0};
+      if (left >= 4) {
+        __builtin_memcpy(&p[u], src, 16);
       } else {
-        const uint16_t* hv = reinterpret_cast<const uint16_t*>(&o);
-        for (int i = 0; i < 8 && c + i < cols; ++i) dst[i] = hv[i];
+        for (int c = 0; c < left; ++c) p[u][c] = src[c];
       }
     }
-    __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);   // the reads are done before the next pass writes
-    __builtin_amdgcn_wave_barrier();
-    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (sp + u < splits) s += p[u];
+  }
+  for (int q = tid; q < rt.rows * rank; q += 256) {
+    float t = 0.0f;
+    for (int sl = 0; sl < slices; sl += 8) {
+      float v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        v[u] = t_part[((int64_t)min(sl + u, slices - 1) * m + rt.row0) * rank + q];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) t += sl + u < slices ? v[u] : 0.0f;
+    }
+    t_lds[q] = t;
+  }
+  const int64_t wrow = (int64_t)rt.group * n;
+  const float sr = xs[row];
+  f32x4 out;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    out[j] = (float)s[j] * fp16_bits_to_f32(scales[wrow + min(c0 + j, n - 1)]) * sr;
+  __syncthreads();
+  if (lrow >= rt.rows || left <= 0) return;
+  for (int r0 = 0; r0 < rank; r0 += 8) {
+    const f32x4 ta = *reinterpret_cast<const f32x4*>(&t_lds[lrow * rank + r0]);
+    const f32x4 tb = *reinterpret_cast<const f32x4*>(&t_lds[lrow * rank + r0 + 4]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const u32x4 u = *reinterpret_cast<const u32x4*>(up + (wrow + min(c0 + j, n - 1)) * rank + r0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float t0 = i < 2 ? ta[2 * i] : tb[2 * i - 4], t1 = i < 2 ? ta[2 * i + 1] : tb[2 * i - 3];
+        out[j] = __builtin_fmaf(t0, __uint_as_float(u[i] << 16), out[j]);
+        out[j] = __builtin_fmaf(t1, __uint_as_float(u[i] & 0xFFFF0000u), out[j]);
+      }
+    }
+  }
+  store4(y, (int64_t)row * n + c0, out, left, y_bf16);
+}
+
+// ---------------------------------------------------------------- small tiles
+// 16 MT x 16 NT output tile per workgroup; its waves split K (256-value blocks
+// in turn) and read both operands straight from memory in MFMA order: lane
+// (f, g) holds 16 bytes of row f, K 64 s + 16 g.  With few rows the codes are
+// read once and bound the time; nothing is shared between waves until the
+// int32 partial sums, which meet in LDS (exact, so the split does not show).
+// U of a block's four 64-value steps are in flight while the U before them are
+// contracted.
+template <int MT, int NT, int U>
+__global__ void __launch_bounds__(512) k_w8a8_stream(
+    const int8_t* __restrict__ xq, const float* __restrict__ xs,
+    const float* __restrict__ t_part, const int8_t* __restrict__ codes,
+    const uint16_t* __restrict__ scales, const uint16_t* __restrict__ up,
+    const int32_t* __restrict__ offsets, int groups, void* __restrict__ y, int m, int n, int k,
+    int rank, int slices, int y_bf16) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  constexpr int BM = 16 * MT, BN = 16 * NT;
+  const int tid = threadIdx.x, lane = tid & 63, fr = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int waves = __builtin_amdgcn_readfirstlane((int)(blockDim.x >> 6));
+  const int nt = (n + BN - 1) / BN;
+  const int mt = row_tile_count(offsets, groups, m, BM, lane);
+  if ((int64_t)blockIdx.x >= (int64_t)mt * nt) return;
+  int64_t tm, tn;
+  xcd_tile(blockIdx.x, (int64_t)mt * nt, nt, tm, tn);
+  RowTile rt;
+  if (!find_row_tile(offsets, groups, m, BM, __builtin_amdgcn_readfirstlane((int)tm), lane, rt))
+    return;
+  const int grp = __builtin_amdgcn_readfirstlane(rt.group);
+  const int rows = __builtin_amdgcn_readfirstlane(rt.rows);
+  const int64_t m0 = __builtin_amdgcn_readfirstlane(rt.row0);
+  const int n0 = __builtin_amdgcn_readfirstlane((int)tn) * BN;
+  const int cols = min(BN, n - n0);
+  const int64_t brow0 = (int64_t)grp * n + n0;
+  const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(xq + m0 * k), (short)0, rows * k, 0x00020000);
+  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(codes + brow0 * k), (short)0, cols * k, 0x00020000);
+  uint32_t off_a[MT], off_b[NT];   // rows past the tile repeat its last row
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+    off_a[i] = (uint32_t)min(16 * i + fr, rows - 1) * (uint32_t)k + 16u * g;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    off_b[j] = (uint32_t)min(16 * j + fr, cols - 1) * (uint32_t)k + 16u * g;
+
+  struct Steps {
+    i32x4 a[U][MT], b[U][NT];
+  };
+  const int nb = k >> 8;
+  constexpr int PER = 4 / U;                       // groups of U steps per block
+  const int todo = (nb - wave + waves - 1) / waves * PER;   // of this wave
+  auto load = [&](Steps& f, int q) {
+    // group q of this wave: block wave + waves (q / PER), steps U (q % PER) ..
+    const int at = (wave + waves * (q / PER)) * 256 + 64 * U * (q % PER);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        f.b[u][j] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(b_rsrc, off_b[j], at + 64 * u, 0));
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        f.a[u][i] = __builtin_bit_cast(
+            i32x4, __builtin_amdgcn_raw_buffer_load_b128(a_rsrc, off_a[i], at + 64 * u, 0));
+    }
+  };
+  i32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
+  auto compute = [&](const Steps& f) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[u][i], f.b[u][j], acc[i][j], 0, 0, 0);
+  };
+  Steps f0, f1;
+  if (todo > 0) load(f0, 0);
+  int q = 0;
+  for (; q + 2 <= todo; q += 2) {
+    load(f1, q + 1);
+    compute(f0);
+    if (q + 2 < todo) load(f0, q + 2);
+    compute(f1);
+  }
+  if (q < todo) compute(f0);
+
+  // t parts of the rows: part, eight ranks, row -> 16 bytes; then the sums
+  const int rank8 = rank >> 3, parts = y_bf16 ? 2 : 3;
+  uint8_t* t_lds = dyn;
+  uint8_t* red = dyn + (size_t)3 * rank8 * BM * 16;
+  for (int c = tid; c < BM * rank8; c += blockDim.x) {
+    const int row = c % BM, r8 = c / BM;
+    u32x4 part[3];
+    project_sum8(t_part, m, rank, slices, (int)m0 + min(row, rows - 1), 8 * r8, part);
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+      *reinterpret_cast<u32x4*>(t_lds + ((p * rank8 + r8) * BM + row) * 16) = part[p];
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      *reinterpret_cast<i32x4*>(red + ((wave * MT + i) * NT + j) * 1024 + lane * 16) = acc[i][j];
+  __syncthreads();
+  // 16 x 16 tiles in turn: row 16 i + 4 g + v, column 16 j + fr
+  for (int tile = wave; tile < MT * NT; tile += waves) {
+    const int i = tile / NT, j = tile % NT;
+    i32x4 s = {0, 0, 0, 0};
+    for (int w = 0; w < waves; ++w)
+      s += *reinterpret_cast<const i32x4*>(red + (w * MT * NT + tile) * 1024 + lane * 16);
+    const int col = 16 * j + fr;
+    const int64_t wrow = brow0 + min(col, cols - 1);
+    const float wsc = fp16_bits_to_f32(scales[wrow]);
+    f32x4 out;
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+      out[v] = (float)s[v] * wsc * xs[m0 + min(16 * i + 4 * g + v, rows - 1)];
+    for (int rr = 0; rr < rank8; rr += 4) {
+      const bool rk = rr + g < rank8;
+      const bf16x8 bu =
+          rk ? *reinterpret_cast<const bf16x8*>(up + wrow * rank + 8 * (rr + g)) : (bf16x8){};
+      for (int p = 0; p < parts; ++p) {
+        const bf16x8 at = rk ? *reinterpret_cast<const bf16x8*>(
+                                   t_lds + ((p * rank8 + rr + g) * BM + 16 * i + fr) * 16)
+                             : (bf16x8){};
+        out = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at, bu, out, 0, 0, 0);
+      }
+    }
+    if (col >= cols) continue;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const int r = 16 * i + 4 * g + v;
+      if (r >= rows) continue;
+      const int64_t at = (m0 + r) * n + n0 + col;
+      if (y_bf16)
+        reinterpret_cast<uint16_t*>(y)[at] = f32_to_bf16(out[v]);
+      else
+        reinterpret_cast<float*>(y)[at] = out[v];
+    }
   }
 }
 
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+// Tile of the contraction.  Each form's time (us) is modelled and the least
+// chosen; the constants are fitted to 3500 timed (M, N, K, groups) between
+// 1 x 64 x 256 and 16384 x 4096 x 4096 / 4480 x 16384 x 16384, over which the
+// choice takes 1.03 times the best form on average.  What decides:
+//   small tiles (waves split K, operands straight from memory): the time grows
+//     with the K steps of a wave and with the tiles per CU; 16 x 32 reads the
+//     codes once for up to 16 rows (1 x 16384 x 6144: 25 us against 34 us for
+//     a 64 x 256 tile with 4 splits) and 64 x 64 shares them among more rows
+//     (777 x 1003 x 2304: 22 against 27 us);
+//   large tiles (operands shared in LDS): whole rounds of 256 tiles, one stage
+//     of 128 K after another; few tiles split K so that every CU has one (48 x
+//     6144 x 16384: 38 us with 8 splits, 175 us with one), at the price of the
+//     partial sums' trip through memory.
+struct SmallTile {
+  int mt, nt;
+  double fixed, step, share;     // us, us per K step of a wave, us per step and tile per CU
+};
+constexpr SmallTile kSmall[] = {
+    {1, 1, 7.5, 1.63, 0.84}, {1, 2, 6.4, 3.0, 2.5}, {2, 4, 7.0, 4.9, 4.5}, {4, 4, 11.2, 4.1, 6.7}};
+struct LargeTile {
+  int rows;
+  double fixed, tile, stage;     // us, us per round, us per stage and round
+  bool split;
+  double join, bytes;            // join: us, and MB of partial sums per us
+};
+constexpr LargeTile kLarge[] = {{64, 5.2, 6.8, 0.82, true, 6.2, 1.4},
+                                {128, 9.4, 5.3, 0.96, true, 4.1, 1.5},
+                                {224, 0.0, 15.5, 0.95, false, 0, 1},
+                                {256, 0.0, 14.8, 1.52, false, 0, 1}};
+
+// Row tiles to expect: groups end inside a tile.
+double expected_tiles(int64_t m, int groups, int tile_m) {
+  if (groups <= 1) return (double)((m + tile_m - 1) / tile_m);
+  const double used = (double)std::min<int64_t>(groups, m);
+  return used * std::max(1.0, (double)m / used / tile_m + 0.4);
+}
+
+void choose_tile(W8A8Plan& p) {
+  const int64_t nb = p.k / 256;
+  double best = 1e30;
+  p.splits = 1;
+  p.waves = (int)std::min<int64_t>(nb, 8);
+  for (const SmallTile& t : kSmall) {
+    const double tiles = expected_tiles(p.m, p.groups, 16 * t.mt) *
+                         (double)((p.n + 16 * t.nt - 1) / (16 * t.nt));
+    const double us = t.fixed + (double)((nb + 7) / 8) * (t.step + t.share * tiles / 256.0);
+    if (us < best) {
+      best = us;
+      p.tile_m = 16 * t.mt;
+      p.tile_n = 16 * t.nt;
+    }
+  }
+  for (const LargeTile& t : kLarge) {
+    const double tiles = expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN);
+    for (int s : {1, 2, 3, 4, 6, 8, 12}) {
+      if (s > nb || (s > 1 && !t.split)) break;
+      const double rounds = p.groups > 1 ? std::max(1.0, tiles * s / 256.0 + 0.3)
+                                         : std::ceil(tiles * s / 256.0);
+      double us = t.fixed + rounds * (t.tile + t.stage * (double)p.k / 128.0 / s);
+      if (s > 1) us += t.join + (double)p.m * (double)p.n * s * 4e-6 / t.bytes;
+      if (us < best) {
+        best = us;
+        p.tile_m = t.rows;
+        p.tile_n = G_BN;
+        p.splits = s;
+      }
+    }
+  }
+}
 
 }  // namespace
 
@@ -421,11 +774,13 @@ W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank) {
   }
   p.prep_rows = rows;
   p.prep_waves = waves;
+  choose_tile(p);
   p.slices = rank ? i8_project_slices(i8_tile_bound(m, groups, 16), k, waves) : 0;
   size_t off = 0;
   p.off_xq = off; off = align256(off + (size_t)m * k);
   p.off_xs = off; off = align256(off + (size_t)m * 4);
   p.off_t = off;  off = align256(off + (size_t)p.slices * m * rank * 4);
+  p.off_part = off; off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * n * 4 : 0));
   p.total = off;
   return p;
 }
@@ -453,9 +808,42 @@ hipError_t launch_w8a8(const W8A8Plan& p, const uint16_t* x, const int32_t* offs
 #undef SQ_W8A8_PREP
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
-  const int64_t tiles = i8_tile_bound(p.m, p.groups, G_BM) * ((p.n + G_BN - 1) / G_BN);
-  hipLaunchKernelGGL(k_w8a8_gemm, dim3((unsigned)tiles), dim3(G_THREADS), 0, stream, xq, xs, t,
-                     codes, scales, up, offsets, p.groups, y, m, n, k, p.rank, p.slices, y_bf16);
+  const int64_t tiles =
+      i8_tile_bound(p.m, p.groups, p.tile_m) * ((p.n + p.tile_n - 1) / p.tile_n);
+  if (p.tile_n < G_BN) {
+    const size_t slds = (size_t)3 * (p.rank / 8) * p.tile_m * 16 +
+                        (size_t)p.waves * (p.tile_m / 16) * (p.tile_n / 16) * 1024;
+#define SQ_W8A8_STREAM(MT, NT, U)                                                                 \
+  hipLaunchKernelGGL((k_w8a8_stream<MT, NT, U>), dim3((unsigned)tiles), dim3(64 * p.waves), slds, \
+                     stream, xq, xs, t, codes, scales, up, offsets, p.groups, y, m, n, k, p.rank, \
+                     p.slices, y_bf16)
+    if (p.tile_n == 16) SQ_W8A8_STREAM(1, 1, 4);
+    else if (p.tile_m == 16) SQ_W8A8_STREAM(1, 2, 4);
+    else if (p.tile_m == 32) SQ_W8A8_STREAM(2, 4, 2);
+    else SQ_W8A8_STREAM(4, 4, 2);
+#undef SQ_W8A8_STREAM
+    return hipGetLastError();
+  }
+  int32_t* part = reinterpret_cast<int32_t*>(base + p.off_part);
+#define SQ_W8A8_GEMM(FM, SPLIT)                                                                    \
+  hipLaunchKernelGGL((k_w8a8_gemm<FM, SPLIT>), dim3((unsigned)(tiles * p.splits)), dim3(G_THREADS), 0,    \
+                     stream, xq, xs, t, codes, scales, up, offsets, p.groups, y, m, n, k, p.rank,  \
+                     p.slices, y_bf16, p.splits, part)
+  if (p.splits > 1) {
+    if (p.tile_m == 128) SQ_W8A8_GEMM(4, true);
+    else SQ_W8A8_GEMM(2, true);
+  } else if (p.tile_m == 256) SQ_W8A8_GEMM(8, false);
+  else if (p.tile_m == 224) SQ_W8A8_GEMM(7, false);
+  else if (p.tile_m == 128) SQ_W8A8_GEMM(4, false);
+  else SQ_W8A8_GEMM(2, false);
+#undef SQ_W8A8_GEMM
+  if (p.splits > 1) {
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    hipLaunchKernelGGL(k_w8a8_join,
+                       dim3((unsigned)(i8_tile_bound(p.m, p.groups, 16) * ((p.n + 63) / 64))),
+                       dim3(256), 0, stream, part, xs, t, scales, up, offsets, p.groups, y, m, n,
+                       p.rank, p.slices, y_bf16, p.splits);
+  }
   return hipGetLastError();
 }
 

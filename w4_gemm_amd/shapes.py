@@ -11,7 +11,7 @@ from __future__ import annotations
 
 
 def _shape(s) -> tuple:
-    return tuple(int(v) for v in s)
+    return s if isinstance(s, tuple) else tuple(int(v) for v in s)
 
 
 def _need(name: str, got, want) -> None:

@@ -96,6 +96,24 @@ __device__ __forceinline__ int group_of_row(const int32_t* __restrict__ offsets,
   return e < groups ? e : -1;
 }
 
+// ---------------------------------------------------------------- last round
+// Tiles run in rounds of one per CU.  The tiles past the last whole round are
+// cut along the contraction into up to max_split parts each, so that they fill
+// the chip too; the parts' integer sums are joined by a second kernel.
+constexpr int I8_CUS = 256;
+struct Tail {
+  int full, splits;   // tiles before the tail; parts per tail tile (1: no split)
+};
+__host__ __device__ __forceinline__ Tail tile_tail(int tiles, int max_split) {
+  const int rem = tiles % I8_CUS;
+  int s = rem > 0 ? I8_CUS / rem : 1;
+  s = s < max_split ? s : max_split;
+  Tail t;
+  t.splits = s > 1 ? s : 1;
+  t.full = t.splits > 1 ? tiles - rem : tiles;
+  return t;
+}
+
 // Eight consecutive 16-bit values from a 2-byte aligned address (one load:
 // the hardware takes unaligned vector loads); values at or past `left` read
 // as zero and are not touched in memory.
@@ -111,14 +129,17 @@ __device__ __forceinline__ u32x4 load8_u16(const uint16_t* __restrict__ p, int l
 
 // ---------------------------------------------------------------- rank-r projection
 // t_part[slice][row][r] = sum over the slice's columns of a[row][c] fac[c][r]
-// for the 16 rows of one tile: a bf16 [m][cols], fac bf16 [cols][rank] (the
+// for the 16 RW rows of one tile: a bf16 [m][cols], fac bf16 [cols][rank] (the
 // group's factor), exact products and fp32 sums on bf16 MFMA.  The workgroup's
-// waves take the slice's 256-column blocks in turn and their sums are added
-// in wave order, so the result does not depend on timing.  Each wave stages
-// 32 factor rows in its own LDS (2 * 32 * rank bytes) and reads them
-// transposed (eight consecutive c of one rank column per lane).
+// waves take the slice's 256-column blocks in turn and their sums are added in
+// wave order, so the result does not depend on timing.  Each wave stages 32
+// factor rows at a time in its own LDS (64 rank bytes) and reads them
+// transposed (eight consecutive c of one rank column per lane); the loads of
+// the next 32 columns are in flight meanwhile.  RW = 2 reads the factor once
+// for 32 rows; RW = 1 gives few rows to more workgroups.
+// VEC: cols is a multiple of eight and a is 16-byte aligned.
 // mem: dynamic LDS, 64 * rank bytes per wave (also holds the partial sums).
-template <int RANK>
+template <int RANK, int RW, bool VEC>
 __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
                                              const uint16_t* __restrict__ fac,
                                              float* __restrict__ t_part, uint8_t* mem, int m,
@@ -130,64 +151,117 @@ __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
   const int b0 = (int)((int64_t)slice * blocks / slices);
   const int b1 = (int)((int64_t)(slice + 1) * blocks / slices);
   uint8_t* stage = mem + wave * 64 * RANK;
-  const uint16_t* arow = a + (int64_t)(rt.row0 + min(fr, rt.rows - 1)) * cols;
-  f32x4 acc[RT] = {};
-  for (int b = b0 + wave; b < b1; b += waves) {
-#pragma unroll 2
-    for (int s = 0; s < 8; ++s) {
-      const int c0 = b * 256 + 32 * s;
-      if (c0 >= cols) break;
-      const u32x4 av = load8_u16(arow + c0 + 8 * g, cols - (c0 + 8 * g));
-      // 32 factor rows of RANK values: RANK / 16 chunks of 16 bytes per lane
-      u32x4 fv[RT];
+  const uint16_t* arow[RW];   // rows past the tile repeat its last row
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const int q = 64 * j + lane;             // 16-byte chunk of the 32 rows
-        const int c = c0 + q / (RANK / 8);
-        fv[j] = (u32x4){0u, 0u, 0u, 0u};
-        if (c < cols)
-          fv[j] = *reinterpret_cast<const u32x4*>(fac + (int64_t)c * RANK + 8 * (q % (RANK / 8)));
+  for (int i = 0; i < RW; ++i)
+    arow[i] = a + (int64_t)(rt.row0 + min(16 * i + fr, rt.rows - 1)) * cols;
+  struct Step {
+    u32x4 a[RW], f[RT];
+  };
+  const int steps = max(b1 - b0 - wave + waves - 1, 0) / waves * 8;   // 32 columns each
+  auto load = [&](Step& st, int q) {
+    const int c0 = (b0 + wave + waves * (q >> 3)) * 256 + 32 * (q & 7);
+    const int ca = c0 + 8 * g;
+#pragma unroll
+    for (int i = 0; i < RW; ++i) {
+      if constexpr (VEC) {
+        st.a[i] = (u32x4){0u, 0u, 0u, 0u};
+        if (ca < cols) st.a[i] = *reinterpret_cast<const u32x4*>(arow[i] + ca);
+      } else {
+        st.a[i] = load8_u16(arow[i] + ca, cols - ca);
       }
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-        *reinterpret_cast<u32x4*>(stage + 16 * (64 * j + lane)) = fv[j];
-      __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
-      __builtin_amdgcn_wave_barrier();
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
-#pragma unroll
-      for (int rt16 = 0; rt16 < RT; ++rt16) {
-        // transposed reads of four rows each: lane 4j + q of a 16-lane group
-        // points at row j, columns 4q..4q+3; lane i receives column i
-        s16x4 h[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int row = 8 * g + 4 * u + (fr >> 2), col = 16 * rt16 + 4 * (fr & 3);
-          h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(stage + 2 * (row * RANK + col)));
-        }
-        typedef short s16x8 __attribute__((ext_vector_type(8)));
-        const s16x8 bv = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
-        acc[rt16] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, av),
-                                                            __builtin_bit_cast(bf16x8, bv),
-                                                            acc[rt16], 0, 0, 0);
-      }
-      __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);   // the reads are done before the next write
-      __builtin_amdgcn_wave_barrier();
-      __atomic_signal_fence(__ATOMIC_SEQ_CST);
     }
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int q16 = 64 * j + lane;             // 16-byte chunk of the 32 rows
+      const int c = c0 + q16 / (RANK / 8);
+      st.f[j] = (u32x4){0u, 0u, 0u, 0u};
+      if (c < cols)
+        st.f[j] = *reinterpret_cast<const u32x4*>(fac + (int64_t)c * RANK + 8 * (q16 % (RANK / 8)));
+    }
+  };
+  f32x4 acc[RW][RT];
+#pragma unroll
+  for (int i = 0; i < RW; ++i)
+#pragma unroll
+    for (int j = 0; j < RT; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto use = [&](const Step& st) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+      *reinterpret_cast<u32x4*>(stage + 16 * (64 * j + lane)) = st.f[j];
+    __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
+    __builtin_amdgcn_wave_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    s16x8 bv[RT];
+#pragma unroll
+    for (int r16 = 0; r16 < RT; ++r16) {
+      // transposed reads of four rows each: lane 4j + q of a 16-lane group
+      // points at row j, columns 4q..4q+3; lane i receives column i
+      s16x4 h[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int row = 8 * g + 4 * u + (fr >> 2), col = 16 * r16 + 4 * (fr & 3);
+        h[u] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) s16x4*)(stage + 2 * (row * RANK + col)));
+      }
+      bv[r16] = __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+#pragma unroll
+    for (int i = 0; i < RW; ++i)
+#pragma unroll
+      for (int r16 = 0; r16 < RT; ++r16)
+        acc[i][r16] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, st.a[i]), __builtin_bit_cast(bf16x8, bv[r16]), acc[i][r16],
+            0, 0, 0);
+    __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);   // the reads are done before the next write
+    __builtin_amdgcn_wave_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+  };
+  Step s0, s1;
+  if (steps > 0) load(s0, 0);
+  for (int q = 0; q < steps; q += 2) {   // an even number of steps
+    load(s1, q + 1);
+    use(s0);
+    if (q + 2 < steps) load(s0, q + 2);
+    use(s1);
   }
-  // acc[r16][i]: row 4g + i, rank column 16 r16 + fr
+  // acc[i][r16][v]: row 16 i + 4g + v, rank column 16 r16 + fr
   float* red = reinterpret_cast<float*>(stage);
 #pragma unroll
-  for (int r16 = 0; r16 < RT; ++r16)
+  for (int i = 0; i < RW; ++i) {
+    const int left = min(rt.rows - 16 * i, 16);
+    if (left <= 0) break;
+    if (i > 0) __syncthreads();   // the sums of the 16 rows before are read
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[(4 * g + i) * RANK + 16 * r16 + fr] = acc[r16][i];
-  __syncthreads();
-  for (int i = tid; i < rt.rows * RANK; i += blockDim.x) {
-    float t = 0.0f;
-    for (int w = 0; w < waves; ++w) t += reinterpret_cast<const float*>(mem + w * 64 * RANK)[i];
-    t_part[((int64_t)slice * m + rt.row0) * RANK + i] = t;
+    for (int r16 = 0; r16 < RT; ++r16)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) red[(4 * g + v) * RANK + 16 * r16 + fr] = acc[i][r16][v];
+    __syncthreads();
+    for (int e = tid; e < left * RANK; e += blockDim.x) {
+      float t = 0.0f;
+      for (int w = 0; w < waves; ++w) t += reinterpret_cast<const float*>(mem + w * 64 * RANK)[e];
+      t_part[((int64_t)slice * m + rt.row0 + 16 * i) * RANK + e] = t;
+    }
   }
+}
+
+// Workgroup b of the projection: row tile b / slices, slice b % slices.
+template <int RW, bool VEC>
+__device__ __forceinline__ void project(const uint16_t* __restrict__ a,
+                                        const uint16_t* __restrict__ fac,
+                                        const int32_t* __restrict__ offsets, int groups,
+                                        float* __restrict__ t_part, uint8_t* mem, int m, int cols,
+                                        int rank, int b, int slices) {
+  RowTile rt;
+  if (!find_row_tile(offsets, groups, m, 16 * RW, b / slices, threadIdx.x & 63, rt)) return;
+  const uint16_t* f = fac + (int64_t)rt.group * cols * rank;
+  if (rank == 16)
+    project_tile<16, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
+  else if (rank == 32)
+    project_tile<32, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
+  else
+    project_tile<64, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
 }
 
 // t of one row, eight rank columns from r0, summed over the slices in order

@@ -110,7 +110,9 @@ hipError_t launch_dgrad(const DgradPlan& plan, const uint16_t* dy, const uint8_t
 // 8-bit products of the int8 mode.  offsets == null: one layer (groups = 1);
 // else rows offsets[e] .. offsets[e+1]-1 use expert e of stacked payloads.
 int64_t i8_tile_bound(int64_t m, int groups, int tile_m);
-int i8_project_slices(int64_t tiles16, int64_t cols, int waves);
+double i8_expected_tiles(int64_t m, int groups, int tile_m);
+void i8_project_plan(int64_t m, int groups, int64_t cols, int waves, int rank, int* t_rows,
+                     int* slices);
 
 struct W8A8Plan {
   int64_t m, n, k;
@@ -118,7 +120,7 @@ struct W8A8Plan {
   int prep_rows, prep_waves;   // rows and waves of a pre-phase workgroup
   int tile_m, tile_n;          // contraction tile
   int waves;                   // small tiles: waves that split K
-  int slices;                  // K slices of the rank-r projection
+  int t_rows, slices;          // row tile and K slices of the rank-r projection
   int splits;                  // K splits of the contraction
   size_t off_xq, off_xs, off_t, off_part, total;
 };
@@ -129,10 +131,11 @@ hipError_t launch_w8a8(const W8A8Plan& plan, const uint16_t* x, const int32_t* o
                        hipStream_t stream);
 
 struct W8DgradPlan {
-  int64_t m, n, k, npad;       // npad: n rounded up to the 64-row stage
+  int64_t m, n, k, npad;       // npad: n rounded up to two stages of 128
   int groups, rank;
-  int slices;                  // N slices of the rank-r projection
-  size_t off_hi, off_lo, off_ts, off_t, total;
+  int t_rows, slices;          // row tile and N slices of the rank-r projection
+  int tile_m, max_split;       // rows of the contraction tile; parts of a tail tile at most
+  size_t off_d, off_ts, off_t, off_part, total;
 };
 W8DgradPlan plan_w8_dgrad(int64_t m, int64_t n, int64_t k, int groups, int rank);
 hipError_t launch_w8_dgrad(const W8DgradPlan& plan, const uint16_t* dy, const int32_t* offsets,

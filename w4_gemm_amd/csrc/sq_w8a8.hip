@@ -64,31 +64,28 @@ __device__ __forceinline__ void iwht256(int (&v)[64]) {
 constexpr int PREP_MAX_ROWS = 64;   // rows per workgroup at most
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
-// Workgroups 0 .. quant_wgs-1 hold rows_per_wg rows each, four lanes per
-// (row, block) pair, 16 pairs per wave; the rest compute t.
-template <int RANK>
+// The first workgroups compute t (they run longest); the others hold
+// rows_per_wg rows each, four lanes per (row, block) pair, 16 pairs per wave.
+template <int RW>
 __global__ void __launch_bounds__(1024) k_w8a8_prep(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ down,
     const int32_t* __restrict__ offsets, int groups, int8_t* __restrict__ xq,
-    float* __restrict__ xs, float* __restrict__ t_part, int m, int k, int rows_per_wg,
-    int quant_wgs, int slices) {
+    float* __restrict__ xs, float* __restrict__ t_part, int m, int k, int rank, int rows_per_wg,
+    int project_wgs, int slices) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63;
-  if (RANK > 0 && (int)blockIdx.x >= quant_wgs) {
-    const int b = (int)blockIdx.x - quant_wgs;
-    RowTile rt;
-    if (!find_row_tile(offsets, groups, m, 16, b / slices, lane, rt)) return;
-    project_tile<RANK ? RANK : 16>(x, down + (int64_t)rt.group * k * RANK, t_part, dyn, m, k, rt,
-                                   b % slices, slices);
+  if ((int)blockIdx.x < project_wgs) {
+    project<RW, true>(x, down, offsets, groups, t_part, dyn, m, k, rank, blockIdx.x, slices);
     return;
   }
+  const int wg = (int)blockIdx.x - project_wgs;
   __shared__ uint32_t row_max[PREP_MAX_ROWS];
   if (tid < PREP_MAX_ROWS) row_max[tid] = 0;
   __syncthreads();
   const int nb = k >> 8;
   const int pair = (tid >> 6) * 16 + (lane & 15), g = lane >> 4;
   const int lrow = pair / nb, blk = pair - lrow * nb;
-  const int row = (int)blockIdx.x * rows_per_wg + lrow;
+  const int row = wg * rows_per_wg + lrow;
   const bool live = lrow < rows_per_wg && row < m;
   float v[64];
   int e = 0;
@@ -696,30 +693,26 @@ constexpr LargeTile kLarge[] = {{64, 5.2, 6.8, 0.82, true, 6.2, 1.4},
                                 {224, 0.0, 15.5, 0.95, false, 0, 1},
                                 {256, 0.0, 14.8, 1.52, false, 0, 1}};
 
-// Row tiles to expect: groups end inside a tile.
-double expected_tiles(int64_t m, int groups, int tile_m) {
-  if (groups <= 1) return (double)((m + tile_m - 1) / tile_m);
-  const double used = (double)std::min<int64_t>(groups, m);
-  return used * std::max(1.0, (double)m / used / tile_m + 0.4);
-}
-
 void choose_tile(W8A8Plan& p) {
   const int64_t nb = p.k / 256;
   double best = 1e30;
   p.splits = 1;
-  p.waves = (int)std::min<int64_t>(nb, 8);
   for (const SmallTile& t : kSmall) {
-    const double tiles = expected_tiles(p.m, p.groups, 16 * t.mt) *
+    const double tiles = i8_expected_tiles(p.m, p.groups, 16 * t.mt) *
                          (double)((p.n + 16 * t.nt - 1) / (16 * t.nt));
     const double us = t.fixed + (double)((nb + 7) / 8) * (t.step + t.share * tiles / 256.0);
     if (us < best) {
       best = us;
       p.tile_m = 16 * t.mt;
       p.tile_n = 16 * t.nt;
+      // with many tiles per CU two blocks of K per wave hide the loads better
+      // than more waves (128 rows, 64 experts of 2816 x 2048: 61 us with four
+      // waves, 82 us with eight)
+      p.waves = (int)(tiles > 1024 ? std::clamp<int64_t>(nb / 2, 1, 8) : std::min<int64_t>(nb, 8));
     }
   }
   for (const LargeTile& t : kLarge) {
-    const double tiles = expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN);
+    const double tiles = i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN);
     for (int s : {1, 2, 3, 4, 6, 8, 12}) {
       if (s > nb || (s > 1 && !t.split)) break;
       const double rounds = p.groups > 1 ? std::max(1.0, tiles * s / 256.0 + 0.3)
@@ -744,12 +737,24 @@ int64_t i8_tile_bound(int64_t m, int groups, int tile_m) {
   return groups <= 1 ? (m + tile_m - 1) / tile_m : (m + used * (tile_m - 1)) / tile_m;
 }
 
-// K slices of the rank-r projection: enough 16-row tiles x slices to put two
-// workgroups on each of the 256 CUs, at least one 256-column block per wave.
-int i8_project_slices(int64_t tiles16, int64_t cols, int waves) {
-  const int64_t blocks = (cols + 255) / 256;
-  const int64_t most = (blocks + waves - 1) / waves;
-  return (int)std::max<int64_t>(1, std::min(most, (512 + tiles16 - 1) / tiles16));
+// Row tiles to expect of them: groups end inside a tile.
+double i8_expected_tiles(int64_t m, int groups, int tile_m) {
+  if (groups <= 1) return (double)((m + tile_m - 1) / tile_m);
+  const double used = (double)std::max<int64_t>(1, std::min<int64_t>(groups, m));
+  return used * std::max(1.0, (double)m / used / tile_m + 0.4);
+}
+
+// Row tile and K slices of the rank-r projection: 32-row tiles from 64 rows per
+// group on (they read the factor half as often), and enough slices for 4096
+// waves, at least one 256-column block per wave and at most eight (the
+// contraction reads t once per slice).
+void i8_project_plan(int64_t m, int groups, int64_t cols, int waves, int rank, int* t_rows,
+                     int* slices) {
+  const int64_t used = std::max<int64_t>(1, std::min<int64_t>(groups, m));
+  *t_rows = m / used >= 64 ? 32 : 16;
+  const int64_t tiles = i8_tile_bound(m, groups, *t_rows), blocks = (cols + 255) / 256;
+  const int64_t most = std::min<int64_t>((blocks + waves - 1) / waves, tiles < 16 ? 64 : 8);
+  *slices = rank ? (int)std::max<int64_t>(1, std::min(most, 4096 / (tiles * waves) + 1)) : 0;
 }
 
 W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank) {
@@ -766,7 +771,7 @@ W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank) {
     const int64_t r = std::min<int64_t>({16 * w / nb, PREP_MAX_ROWS, m});
     if (r < 1) continue;
     const double use = (double)(r * nb) / (16.0 * w);
-    if (use > best + 1e-9) {
+    if (use > best - 1e-9) {   // of equals the larger: t has few workgroups otherwise
       best = use;
       rows = (int)r;
       waves = w;
@@ -775,7 +780,7 @@ W8A8Plan plan_w8a8(int64_t m, int64_t n, int64_t k, int groups, int rank) {
   p.prep_rows = rows;
   p.prep_waves = waves;
   choose_tile(p);
-  p.slices = rank ? i8_project_slices(i8_tile_bound(m, groups, 16), k, waves) : 0;
+  i8_project_plan(m, groups, k, waves, rank, &p.t_rows, &p.slices);
   size_t off = 0;
   p.off_xq = off; off = align256(off + (size_t)m * k);
   p.off_xs = off; off = align256(off + (size_t)m * 4);
@@ -795,16 +800,14 @@ hipError_t launch_w8a8(const W8A8Plan& p, const uint16_t* x, const int32_t* offs
   float* t = reinterpret_cast<float*>(base + p.off_t);
   const int m = (int)p.m, n = (int)p.n, k = (int)p.k;
   const int64_t qwgs = (p.m + p.prep_rows - 1) / p.prep_rows;
-  const int64_t twgs = i8_tile_bound(p.m, p.groups, 16) * p.slices;
+  const int64_t twgs = i8_tile_bound(p.m, p.groups, p.t_rows) * p.slices;
   const size_t lds = (size_t)p.prep_waves * 64 * p.rank;
-#define SQ_W8A8_PREP(R)                                                                        \
-  hipLaunchKernelGGL((k_w8a8_prep<R>), dim3((unsigned)(qwgs + twgs)),                          \
-                     dim3(64 * p.prep_waves), lds, stream, x, down, offsets, p.groups, xq, xs, \
-                     t, m, k, p.prep_rows, (int)qwgs, p.slices)
-  if (p.rank == 0) SQ_W8A8_PREP(0);
-  else if (p.rank == 16) SQ_W8A8_PREP(16);
-  else if (p.rank == 32) SQ_W8A8_PREP(32);
-  else SQ_W8A8_PREP(64);
+#define SQ_W8A8_PREP(RW)                                                                        \
+  hipLaunchKernelGGL((k_w8a8_prep<RW>), dim3((unsigned)(qwgs + twgs)), dim3(64 * p.prep_waves), \
+                     lds, stream, x, down, offsets, p.groups, xq, xs, t, m, k, p.rank,          \
+                     p.prep_rows, (int)twgs, p.slices)
+  if (p.t_rows == 16) SQ_W8A8_PREP(1);
+  else SQ_W8A8_PREP(2);
 #undef SQ_W8A8_PREP
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;

@@ -168,27 +168,9 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 // that a lane ends up with four consecutive columns and stores them as they
 // are.
 constexpr int G_BN = 256, G_THREADS = 512;
-constexpr int G_STAGE = 256 * 128;
-__shared__ __attribute__((aligned(16))) uint8_t g_a0[G_STAGE];
-__shared__ __attribute__((aligned(16))) uint8_t g_a1[G_STAGE];
-__shared__ __attribute__((aligned(16))) uint8_t g_b0[G_STAGE];
-__shared__ __attribute__((aligned(16))) uint8_t g_b1[G_STAGE];
-__shared__ __attribute__((aligned(16))) float g_xs[256];
-__shared__ __attribute__((aligned(16))) float g_ws[256];
-
 // Swizzle of 128-byte rows.  A loop of nothing but the fragment reads runs
 // 1.9 times as long under c ^ (r & 7) ^ ((r >> 3) & 1), 3.7 times without any.
 __device__ __forceinline__ int g_swz(int r) { return r & 7; }
-
-// t of the tile's rows as bf16 parts (hi, lo and, for fp32 results, a third:
-// 2^-24 of t then) in LDS: part p, eight ranks r8, row -> 16 bytes.
-template <int BM>
-__device__ __forceinline__ uint8_t* t_chunk(int part, int r8, int row, int rank8) {
-  const int at = ((part * rank8 + r8) * BM + row) * 16;
-  // at most 3 * 8 * 256 chunks; the stage buffers are separate objects
-  uint8_t* base = at < G_STAGE ? g_a0 : at < 2 * G_STAGE ? g_a1 : g_b0;
-  return base + (at & (G_STAGE - 1));
-}
 
 // Four consecutive values of a row, fp32 or bf16; `left` columns remain (rows
 // of an odd N are 4- or 2-byte aligned only).
@@ -220,6 +202,19 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ y, int m, int n, int k,
     int rank, int slices, int y_bf16, int splits, int32_t* __restrict__ partial) {
   constexpr int FN = 4, BM = 32 * FM;
+  // A stage holds whole 64-row loads
+  constexpr int A_STAGE = (BM + 63) / 64 * 64 * 128, B_STAGE = G_BN * 128;
+  __shared__ __attribute__((aligned(16))) uint8_t a0[A_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t b0[B_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t b1[B_STAGE];
+  __shared__ __attribute__((aligned(16))) float row_s[SPLIT ? 4 : BM];
+  __shared__ __attribute__((aligned(16))) float col_w[SPLIT ? 4 : G_BN];
+  // t of the tile's rows as bf16 parts (hi, lo and, for fp32 results, a third:
+  // 2^-24 of t then), chunk (part, eight ranks, row) of 16 bytes.  Rank 16 has
+  // room of its own and is fetched before the loop; the larger ranks (up to
+  // 3 * 8 * BM chunks) take the weight's stage buffers after it.
+  __shared__ __attribute__((aligned(16))) uint8_t t_early[SPLIT ? 16 : 3 * 2 * BM * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -271,13 +266,42 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
                                                off_b, kb + st * 128, 0, 0);
     }
   };
-  issue(0, g_a0, g_b0);
-  issue(min(1, ST - 1), g_a1, g_b1);
-  // scales of the tile's rows and columns, for the epilogue
-  if (tid < 256)
-    g_xs[tid] = xs[m0 + min(tid, rows - 1)];
-  else
-    g_ws[tid - 256] = fp16_bits_to_f32(scales[brow0 + min(tid - 256, cols - 1)]);
+  issue(0, a0, b0);
+  issue(min(1, ST - 1), a1, b1);
+  const int rank8 = rank >> 3, parts = y_bf16 ? 2 : 3;
+  const int c0 = 64 * wn + 4 * fr, left = cols - c0;   // the lane's four columns
+  auto t_chunk = [&](int part, int r8, int row) -> uint8_t* {
+    const int at = ((part * rank8 + r8) * BM + row) * 16;
+    if (rank8 <= 2) return t_early + at;
+    return at < B_STAGE ? b0 + at : at < 2 * B_STAGE ? b1 + (at - B_STAGE) : a0 + (at - 2 * B_STAGE);
+  };
+  auto fetch_t = [&]() {
+    for (int q = tid; q < BM * rank8; q += G_THREADS) {
+      const int row = q % BM, r8 = q / BM;
+      u32x4 part[3];
+      project_sum8(t_part, m, rank, slices, (int)m0 + min(row, rows - 1), 8 * r8, part);
+#pragma unroll
+      for (int p = 0; p < 3; ++p)
+        if (p < parts) *reinterpret_cast<u32x4*>(t_chunk(p, r8, row)) = part[p];
+    }
+  };
+  bf16x8 bu[FN];   // rows of up, eight ranks at a time
+  auto fetch_up = [&](int rr) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+      bu[j] = rr + g < rank8 ? *reinterpret_cast<const bf16x8*>(
+                                   up + (brow0 + min(c0 + j, cols - 1)) * rank + 8 * (rr + g))
+                             : (bf16x8){};
+  };
+  if constexpr (!SPLIT) {
+    // what the epilogue needs comes in with the first stages
+    if (tid < BM)
+      row_s[tid] = xs[m0 + min(tid, rows - 1)];
+    else if (tid >= 256)
+      col_w[tid - 256] = fp16_bits_to_f32(scales[brow0 + min(tid - 256, cols - 1)]);
+    if (rank8 <= 2) fetch_t();
+    fetch_up(0);
+  }
 
   // fragment addresses: K half h is chunks 4 h .. 4 h + 3
   const uint32_t a_row = (uint32_t)(16 * FM * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
@@ -353,16 +377,16 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     __builtin_amdgcn_sched_barrier(0);
   };
   sync();
-  read(f0, g_a0, g_b0, 0);
+  read(f0, a0, b0, 0);
   for (int st = 0; st < ST; st += 2) {
-    stage(st, g_a0, g_b0, g_a1, g_b1);
-    stage(st + 1, g_a1, g_b1, g_a0, g_b0);
+    stage(st, a0, b0, a1, b1);
+    stage(st + 1, a1, b1, a0, b0);
   }
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
   __builtin_amdgcn_sched_barrier(0);
 
   // acc[i][j][v] is row 16 (FM wm + i) + 4 g + v, column 64 wn + 4 fr + j
-  const int rbase = 16 * FM * wm, c0 = 64 * wn + 4 * fr, left = cols - c0;
+  const int rbase = 16 * FM * wm;
   if constexpr (SPLIT) {
     // the splits' integer sums meet in k_w8a8_join
     int32_t* dst = partial + ((int64_t)split * m + m0) * n + n0 + c0;
@@ -381,51 +405,36 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
       }
     return;
   }
-  const int rank8 = rank >> 3, parts = y_bf16 ? 2 : 3;
-  if (rank > 0) {
+  if (rank8 > 2) {
     __syncthreads();   // every wave is done with the stage buffers
-    for (int q = tid; q < BM * rank8; q += G_THREADS) {
-      const int row = q % BM, r8 = q / BM;
-      u32x4 part[3];
-      project_sum8(t_part, m, rank, slices, (int)m0 + min(row, rows - 1), 8 * r8, part);
-#pragma unroll
-      for (int p = 0; p < 3; ++p)
-        if (p < parts) *reinterpret_cast<u32x4*>(t_chunk<BM>(p, r8, row, rank8)) = part[p];
-    }
+    fetch_t();
+    __syncthreads();
   }
   // scales, the column's first: |acc w| < 2^47 cannot overflow whatever the
   // row's magnitude is
   f32x4 out[FM][FN];
-  const f32x4 wsc = *reinterpret_cast<const f32x4*>(&g_ws[c0]);
+  const f32x4 wsc = *reinterpret_cast<const f32x4*>(&col_w[c0]);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const f32x4 sr = *reinterpret_cast<const f32x4*>(&g_xs[rbase + 16 * i + 4 * g]);
+    const f32x4 sr = *reinterpret_cast<const f32x4*>(&row_s[rbase + 16 * i + 4 * g]);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) out[i][j][v] = (float)acc[i][j][v] * wsc[j] * sr[v];
   }
   // rank-r branch t up^T (rank 16: the upper half of the 32-wide step reads zeros)
-  if (rank > 0) {
-    __syncthreads();
-    for (int rr = 0; rr < rank8; rr += 4) {
-      const bool rk = rr + g < rank8;
-      bf16x8 bu[FN];
+  for (int rr = 0; rr < rank8; rr += 4) {
+    const bool rk = rr + g < rank8;
+    if (rr > 0) fetch_up(rr);
+    for (int p = 0; p < parts; ++p) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
-        bu[j] = rk ? *reinterpret_cast<const bf16x8*>(
-                         up + (brow0 + min(c0 + j, cols - 1)) * rank + 8 * (rr + g))
-                   : (bf16x8){};
-      for (int p = 0; p < parts; ++p) {
+      for (int i = 0; i < FM; ++i) {
+        const bf16x8 at = rk ? *reinterpret_cast<const bf16x8*>(
+                                   t_chunk(p, rr + g, rbase + 16 * i + fr))
+                             : (bf16x8){};
 #pragma unroll
-        for (int i = 0; i < FM; ++i) {
-          const bf16x8 at = rk ? *reinterpret_cast<const bf16x8*>(
-                                     t_chunk<BM>(p, rr + g, rbase + 16 * i + fr, rank8))
-                               : (bf16x8){};
-#pragma unroll
-          for (int j = 0; j < FN; ++j)
-            out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at, bu[j], out[i][j], 0, 0, 0);
-        }
+        for (int j = 0; j < FN; ++j)
+          out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at, bu[j], out[i][j], 0, 0, 0);
       }
     }
   }
@@ -746,14 +755,15 @@ double i8_expected_tiles(int64_t m, int groups, int tile_m) {
 
 // Row tile and K slices of the rank-r projection: 32-row tiles from 64 rows per
 // group on (they read the factor half as often), and enough slices for 4096
-// waves, at least one 256-column block per wave and at most eight (the
-// contraction reads t once per slice).
+// waves, at least one 256-column block per wave and at most four (the
+// contraction reads t once per slice: two slices instead of eight take 9 us off
+// 4480 x 16384 x 6144), except for the few tiles of small calls.
 void i8_project_plan(int64_t m, int groups, int64_t cols, int waves, int rank, int* t_rows,
                      int* slices) {
   const int64_t used = std::max<int64_t>(1, std::min<int64_t>(groups, m));
   *t_rows = m / used >= 64 ? 32 : 16;
   const int64_t tiles = i8_tile_bound(m, groups, *t_rows), blocks = (cols + 255) / 256;
-  const int64_t most = std::min<int64_t>((blocks + waves - 1) / waves, tiles < 16 ? 64 : 8);
+  const int64_t most = std::min<int64_t>((blocks + waves - 1) / waves, tiles < 16 ? 64 : 4);
   *slices = rank ? (int)std::max<int64_t>(1, std::min(most, 4096 / (tiles * waves) + 1)) : 0;
 }
 

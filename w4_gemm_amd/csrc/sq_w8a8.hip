@@ -673,9 +673,9 @@ __global__ void __launch_bounds__(512) k_w8a8_stream(
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Tile of the contraction.  Each form's time (us) is modelled and the least
-// chosen; the constants are fitted to 3500 timed (M, N, K, groups) between
+// chosen; the constants are fitted to 6400 timed (M, N, K, groups) between
 // 1 x 64 x 256 and 16384 x 4096 x 4096 / 4480 x 16384 x 16384, over which the
-// choice takes 1.03 times the best form on average.  What decides:
+// choice takes 1.017 times the best form on average.  What decides:
 //   small tiles (waves split K, operands straight from memory): the time grows
 //     with the K steps of a wave and with the tiles per CU; 16 x 32 reads the
 //     codes once for up to 16 rows (1 x 16384 x 6144: 25 us against 34 us for
@@ -687,45 +687,50 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 //     partial sums' trip through memory.
 struct SmallTile {
   int mt, nt;
-  double fixed, step, share;     // us, us per K step of a wave, us per step and tile per CU
+  double fixed, step, share, enough, tile;
 };
-constexpr SmallTile kSmall[] = {
-    {1, 1, 7.5, 1.63, 0.84}, {1, 2, 6.4, 3.0, 2.5}, {2, 4, 7.0, 4.9, 4.5}, {4, 4, 11.2, 4.1, 6.7}};
+constexpr SmallTile kSmall[] = {{1, 1, 7.8, 1.15, 2.2, 0.0, 0.1},
+                                {1, 2, 8.4, 1.7, 3.0, 0.0, 0.3},
+                                {2, 4, 12.0, 3.0, 6.0, 0.3, 0.6},
+                                {4, 4, 11.6, 5.2, 8.8, 0.5, 2.1}};
 struct LargeTile {
   int rows;
   double fixed, tile, stage;     // us, us per round, us per stage and round
-  bool split;
-  double join, bytes;            // join: us, and MB of partial sums per us
+  double join, bytes, parts;     // join: us, MB of partial sums per us, rounds of parts count more
 };
-constexpr LargeTile kLarge[] = {{64, 5.2, 6.8, 0.82, true, 6.2, 1.4},
-                                {128, 9.4, 5.3, 0.96, true, 4.1, 1.5},
-                                {224, 0.0, 15.5, 0.95, false, 0, 1},
-                                {256, 0.0, 14.8, 1.52, false, 0, 1}};
+constexpr LargeTile kLarge[] = {{64, 7.1, 4.5, 0.77, 6.3, 2.6, 1.4},
+                                {128, 8.2, 7.5, 0.9, 7.8, 1.6, 1.0},
+                                {224, 0.0, 19.3, 1.0, 0, 0, 0},
+                                {256, 0.0, 20.7, 1.07, 0, 0, 0}};
 
 void choose_tile(W8A8Plan& p) {
   const int64_t nb = p.k / 256;
   double best = 1e30;
   p.splits = 1;
   for (const SmallTile& t : kSmall) {
+    // tiles per CU; with many of them two blocks of K per wave hide the loads
+    // better than more waves (128 rows, 64 experts of 2816 x 2048: 61 us with
+    // four waves, 82 us with eight)
     const double tiles = i8_expected_tiles(p.m, p.groups, 16 * t.mt) *
-                         (double)((p.n + 16 * t.nt - 1) / (16 * t.nt));
-    const double us = t.fixed + (double)((nb + 7) / 8) * (t.step + t.share * tiles / 256.0);
+                         (double)((p.n + 16 * t.nt - 1) / (16 * t.nt)) / 256.0;
+    const int64_t waves =
+        tiles > 4 ? std::clamp<int64_t>(nb / 2, 1, 8) : std::min<int64_t>(nb, 8);
+    const double us = t.fixed + t.step * (double)((nb + waves - 1) / waves) +
+                      t.share * std::max(0.0, tiles - t.enough) * (double)nb / 8.0 + t.tile * tiles;
     if (us < best) {
       best = us;
       p.tile_m = 16 * t.mt;
       p.tile_n = 16 * t.nt;
-      // with many tiles per CU two blocks of K per wave hide the loads better
-      // than more waves (128 rows, 64 experts of 2816 x 2048: 61 us with four
-      // waves, 82 us with eight)
-      p.waves = (int)(tiles > 1024 ? std::clamp<int64_t>(nb / 2, 1, 8) : std::min<int64_t>(nb, 8));
+      p.waves = (int)waves;
     }
   }
   for (const LargeTile& t : kLarge) {
-    const double tiles = i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN);
+    const double tiles =
+        i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN) / 256.0;
     for (int s : {1, 2, 3, 4, 6, 8, 12}) {
-      if (s > nb || (s > 1 && !t.split)) break;
-      const double rounds = p.groups > 1 ? std::max(1.0, tiles * s / 256.0 + 0.3)
-                                         : std::ceil(tiles * s / 256.0);
+      if (s > nb || (s > 1 && t.bytes == 0)) break;
+      double rounds = p.groups > 1 ? std::max(1.0, tiles * s + 0.3) : std::ceil(tiles * s);
+      if (s > 1) rounds *= t.parts;
       double us = t.fixed + rounds * (t.tile + t.stage * (double)p.k / 128.0 / s);
       if (s > 1) us += t.join + (double)p.m * (double)p.n * s * 4e-6 / t.bytes;
       if (us < best) {

@@ -21,6 +21,7 @@
 //   k_w8_dgrad_join  the same end for the sums of several N splits
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "sq_i8.hpp"
 #include "sq_kernels.h"
@@ -233,57 +234,18 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
   issue(2, d_buf2);
   issue(3, d_buf3);
 
-  // fragments: hi chunks g, lo chunks 4 + g of row fr; transposed read u of
+  // fragments (16-row tile i of wave row wm is tile 2 i + wm of the workgroup):
+  // hi chunks g, lo chunks 4 + g of row fr; transposed read u of
   // column tile j: row 16 g + 8 u + fr / 2, columns 64 wn + 16 j + 8 (fr & 1)
-  const uint32_t a_row = (uint32_t)(16 * FM * wm + fr) * 128;
+  const uint32_t a_row = (uint32_t)(16 * wm + fr) * 128;
   const int tr_row = 16 * g + (fr >> 1);
   const uint32_t b_row = D_B + (uint32_t)tr_row * 256 + 8u * (uint32_t)(fr & 1);
   const int tr_swz = b_swz(tr_row);
-  struct Frag {
-    i32x4 h[FM], l[FM], b[FN];
-  };
-  auto read = [&](Frag& f, const uint8_t* buf) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      i32x2 p[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        p[u] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-            (__attribute__((address_space(3))) i32x2*)(buf + b_row + u * 2048 +
-                                                       16 * ((4 * wn + j) ^ tr_swz)));
-      f.b[j] = (i32x4){p[0][0], p[0][1], p[1][0], p[1][1]};
-    }
-#pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      f.h[i] = *reinterpret_cast<const i32x4*>(buf + a_row + i * 2048 + 16 * (g ^ (fr & 7)));
-      f.l[i] = *reinterpret_cast<const i32x4*>(buf + a_row + i * 2048 + 16 * ((4 + g) ^ (fr & 7)));
-    }
-  };
   i32x4 ah[FM][FN], al[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) ah[i][j] = al[i][j] = (i32x4){0, 0, 0, 0};
-  auto compute = [&](const Frag& f) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        ah[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.h[i], f.b[j], ah[i][j], 0, 0, 0);
-        al[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.l[i], f.b[j], al[i][j], 0, 0, 0);
-      }
-  };
-  // 2 FM + 8 LDS reads and four global loads among 8 FM MFMAs
-  auto interleave = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FM, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FM, 0);
-    }
-  };
   auto sync = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(sq_wait_vm(2 * LOADS));
@@ -291,29 +253,79 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // One stage: stage s sits in registers; at the barrier every wave has read
-  // it, so its buffer takes stage s + 4, and stage s + 1 has landed (the two
-  // after it are still on their way); the fragments of stage s + 1 are read
-  // under the MFMAs of stage s.  Loads past the last stage fetch the last one
-  // again, into buffers that are not read any more.
-  auto step = [&](int s, const Frag& cur, Frag& nxt, uint8_t* buf, const uint8_t* next) {
-    sync();
-    issue(min(s + 4, ST - 1), buf);
-    read(nxt, next);
-    compute(cur);
-    interleave();
-  };
-  Frag f0, f1;
   __builtin_amdgcn_s_waitcnt(sq_wait_vm(3 * LOADS));
   __builtin_amdgcn_s_barrier();
   __builtin_amdgcn_sched_barrier(0);
-  read(f0, d_buf0);
-  for (int s = 0; s < ST; s += 4) {
-    step(s, f0, f1, d_buf0, d_buf1);
-    step(s + 1, f1, f0, d_buf1, d_buf2);
-    step(s + 2, f0, f1, d_buf2, d_buf3);
-    step(s + 3, f1, f0, d_buf3, d_buf0);
-  }
+  // the loop over the first F of the wave's FM row tiles
+  auto contract = [&](auto count) {
+    constexpr int F = decltype(count)::value;
+    struct Frag {
+      i32x4 h[F], l[F], b[FN];
+    };
+    auto read = [&](Frag& f, const uint8_t* buf) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        i32x2 p[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          p[u] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (__attribute__((address_space(3))) i32x2*)(buf + b_row + u * 2048 +
+                                                         16 * ((4 * wn + j) ^ tr_swz)));
+        f.b[j] = (i32x4){p[0][0], p[0][1], p[1][0], p[1][1]};
+      }
+#pragma unroll
+      for (int i = 0; i < F; ++i) {
+        f.h[i] = *reinterpret_cast<const i32x4*>(buf + a_row + i * 4096 + 16 * (g ^ (fr & 7)));
+        f.l[i] = *reinterpret_cast<const i32x4*>(buf + a_row + i * 4096 + 16 * ((4 + g) ^ (fr & 7)));
+      }
+    };
+    auto compute = [&](const Frag& f) {
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          ah[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.h[i], f.b[j], ah[i][j], 0, 0, 0);
+          al[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.l[i], f.b[j], al[i][j], 0, 0, 0);
+        }
+    };
+    // 2 F + 8 LDS reads and four global loads among 8 F MFMAs
+    auto interleave = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, F, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, F, 0);
+      }
+    };
+    // One stage: stage s sits in registers; at the barrier every wave has read
+    // it, so its buffer takes stage s + 4, and stage s + 1 has landed (the two
+    // after it are still on their way); the fragments of stage s + 1 are read
+    // under the MFMAs of stage s.  Loads past the last stage fetch the last one
+    // again, into buffers that are not read any more.
+    auto step = [&](int s, const Frag& cur, Frag& nxt, uint8_t* buf, const uint8_t* next) {
+      sync();
+      issue(min(s + 4, ST - 1), buf);
+      read(nxt, next);
+      compute(cur);
+      interleave();
+    };
+    Frag f0, f1;
+    read(f0, d_buf0);
+    for (int s = 0; s < ST; s += 4) {
+      step(s, f0, f1, d_buf0, d_buf1);
+      step(s + 1, f1, f0, d_buf1, d_buf2);
+      step(s + 2, f0, f1, d_buf2, d_buf3);
+      step(s + 3, f1, f0, d_buf3, d_buf0);
+    }
+  };
+  // a group's last tile is often half empty: it contracts half the row tiles
+  constexpr int HALF = (FM + 1) / 2;
+  if (FM >= 4 && rows <= 32 * HALF)
+    contract(std::integral_constant<int, HALF>{});
+  else
+    contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
   __builtin_amdgcn_sched_barrier(0);
 
@@ -325,7 +337,7 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = 16 * (FM * wm + i) + 4 * g + v;
+        const int r = 32 * i + 16 * wm + 4 * g + v;
         if (r >= rows) continue;
 #pragma unroll
         for (int j = 0; j < FN; ++j)
@@ -338,7 +350,7 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
   // run here, the others after the exchange.
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    uint8_t* st = c_rows((FM * wm + i) >> 1);
+    uint8_t* st = c_rows(i);
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       float c[4];
@@ -346,7 +358,7 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
       for (int j = 0; j < 4; ++j) c[j] = (float)ah[i][j][v] * 256.0f + (float)al[i][j][v];
       const float s0 = c[0] + c[1], s1 = c[0] - c[1], s2 = c[2] + c[3], s3 = c[2] - c[3];
       const float o[4] = {s0 + s2, s1 + s3, s0 - s2, s1 - s3};
-      const int row = 16 * ((FM * wm + i) & 1) + 4 * g + v;
+      const int row = 16 * wm + 4 * g + v;
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         *reinterpret_cast<float*>(st + row * 1024 + 16 * c_unit(row, 16 * wn + 4 * j + (fr >> 2)) +
@@ -388,21 +400,31 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
   // (q, p) is column 64 q + 16 g' + 4 p + i, MFMA column fr the lane's row
   const uint16_t* down0 = down + ((int64_t)grp * k + k0) * rank;
   const int dcol = 16 * (fr >> 2) + (fr & 3);
+  // the 32-wide MFMA takes rank 16 twice: lane groups 0, 1 carry one part of
+  // t, groups 2, 3 the next
+  const bool twice = rank == 16;
   for (int rr = 0; rr < rank; rr += 32) {
-    const bool rk = rr + 8 * g < rank;
+    const int r0 = twice ? 8 * (g & 1) : rr + 8 * g;
     u32x4 part[3] = {};
-    if (rk) project_sum8(t_part, m, rank, slices, rrow, rr + 8 * g, part);
+    project_sum8(t_part, m, rank, slices, rrow, r0, part);
+    if (twice && g >= 2) {
+      part[0] = part[1];
+      part[1] = (u32x4){0u, 0u, 0u, 0u};
+    } else if (twice) {
+      part[1] = part[2];
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
 #pragma unroll
       for (int p = 0; p < 4; ++p) {
-        const uint32_t at = (uint32_t)((64 * q + 4 * p + dcol) * rank + rr + 8 * g);
-        const bf16x8 dv = rk ? *reinterpret_cast<const bf16x8*>(down0 + at) : (bf16x8){};
+        const uint32_t at = (uint32_t)((64 * q + 4 * p + dcol) * rank + r0);
+        const bf16x8 dv = *reinterpret_cast<const bf16x8*>(down0 + at);
         const int b = 16 * q + 4 * p;
         f32x4 acc = {w[b], w[b + 1], w[b + 2], w[b + 3]};
         acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[0]), acc, 0, 0, 0);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[1]), acc, 0, 0, 0);
-        if (!dx_bf16)
+        if (!twice || !dx_bf16)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[1]), acc, 0, 0, 0);
+        if (!twice && !dx_bf16)
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[2]), acc, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[b + i] = acc[i];

@@ -22,6 +22,7 @@
 //                sums below 2^31), scales and rank-r branch in the epilogue
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "sq_i8.hpp"
 #include "sq_kernels.h"
@@ -158,8 +159,11 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 }
 
 // ---------------------------------------------------------------- contraction
-// BM x 256 output tile per workgroup (BM = 32 FM), eight waves of 16 FM x 64
-// (FM x 4 MFMA tiles).  One stage = 128 bytes of K of each operand row, two
+// BM x BN output tile per workgroup (BM = 32 FM, BN = 64 WN), 2 x WN waves of
+// 16 FM x 64 (FM x 4 MFMA tiles).  WN = 4: the operands are shared most.  WN = 2
+// (128 x 128): two workgroups per CU, so that one's loads, scales and stores
+// run under the other's MFMAs; with short K that outweighs the doubled operand
+// traffic.  One stage = 128 bytes of K of each operand row, two
 // stages in LDS.  Both operands stream global -> LDS with direct 16-byte
 // buffer loads that cover whole 128-byte lines (64-byte halves of lines cost
 // 5 % of the 4480 x 16384 x 6144 contraction).  Chunk c of LDS row r sits at
@@ -167,7 +171,6 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 // LDS row 64 w + 16 j + f of the weight holds output column 64 w + 4 f + j, so
 // that a lane ends up with four consecutive columns and stores them as they
 // are.
-constexpr int G_BN = 256, G_THREADS = 512;
 // Swizzle of 128-byte rows.  A loop of nothing but the fragment reads runs
 // 1.9 times as long under c ^ (r & 7) ^ ((r >> 3) & 1), 3.7 times without any.
 __device__ __forceinline__ int g_swz(int r) { return r & 7; }
@@ -194,22 +197,24 @@ __device__ __forceinline__ void store4(void* __restrict__ y, int64_t at, f32x4 o
   }
 }
 
-template <int FM, bool SPLIT>
-__global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
+template <int FM, int WN, bool SPLIT>
+__global__ void __launch_bounds__(128 * WN, 4 / WN) k_w8a8_gemm(
     const int8_t* __restrict__ xq, const float* __restrict__ xs,
     const float* __restrict__ t_part, const int8_t* __restrict__ codes,
     const uint16_t* __restrict__ scales, const uint16_t* __restrict__ up,
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ y, int m, int n, int k,
     int rank, int slices, int y_bf16, int splits, int32_t* __restrict__ partial) {
   constexpr int FN = 4, BM = 32 * FM;
-  // A stage holds whole 64-row loads
-  constexpr int A_STAGE = (BM + 63) / 64 * 64 * 128, B_STAGE = G_BN * 128;
+  constexpr int WAVES = 2 * WN, THREADS = 64 * WAVES, BN = 64 * WN;
+  // one load instruction of every wave covers RR rows of 128 bytes
+  constexpr int RR = 8 * WAVES, NA = (BM + RR - 1) / RR, NB = BN / RR;
+  constexpr int A_STAGE = NA * RR * 128, B_STAGE = BN * 128;
   __shared__ __attribute__((aligned(16))) uint8_t a0[A_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b0[B_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b1[B_STAGE];
   __shared__ __attribute__((aligned(16))) float row_s[SPLIT ? 4 : BM];
-  __shared__ __attribute__((aligned(16))) float col_w[SPLIT ? 4 : G_BN];
+  __shared__ __attribute__((aligned(16))) float col_w[SPLIT ? 4 : BN];
   // t of the tile's rows as bf16 parts (hi, lo and, for fp32 results, a third:
   // 2^-24 of t then), chunk (part, eight ranks, row) of 16 bytes.  Rank 16 has
   // room of its own and is fetched before the loop; the larger ranks (up to
@@ -217,9 +222,9 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   __shared__ __attribute__((aligned(16))) uint8_t t_early[SPLIT ? 16 : 3 * 2 * BM * 16];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / WN, wn = wave % WN;
   const int fr = lane & 15, g = lane >> 4;
-  const int nt = (n + G_BN - 1) / G_BN;
+  const int nt = (n + BN - 1) / BN;
   const int mt = row_tile_count(offsets, groups, m, BM, lane);
   // workgroup b: K split b / tiles of tile b % tiles
   const int tiles = mt * nt;
@@ -234,18 +239,18 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   const int grp = __builtin_amdgcn_readfirstlane(rt.group);
   const int rows = __builtin_amdgcn_readfirstlane(rt.rows);
   const int64_t m0 = __builtin_amdgcn_readfirstlane(rt.row0);
-  const int n0 = __builtin_amdgcn_readfirstlane((int)tn) * G_BN;
-  const int cols = min(G_BN, n - n0);
+  const int n0 = __builtin_amdgcn_readfirstlane((int)tn) * BN;
+  const int cols = min(BN, n - n0);
   const int64_t brow0 = (int64_t)grp * n + n0;   // first weight row of the tile
   // stages of 128 values: an even number (the splits cut K in multiples of 256)
   const int st0 = 2 * __builtin_amdgcn_readfirstlane((int)((int64_t)split * (k >> 8) / splits));
   const int ST =
       2 * __builtin_amdgcn_readfirstlane((int)((int64_t)(split + 1) * (k >> 8) / splits)) - st0;
 
-  // loaders: instruction i of wave w fills LDS rows 64 i + 8 w .. +8, through a
-  // descriptor of its own (64 rows each) so that one offset serves all; rows
-  // past the tile lie beyond their descriptor and fetch nothing
-  constexpr int NA = (BM + 63) / 64;
+  // loaders: instruction i of wave w fills LDS rows RR i + 8 w .. +8, through a
+  // descriptor of its own so that one offset serves all; rows past the tile lie
+  // beyond their descriptor and fetch nothing.  Weight row RR i + lr of the
+  // stage holds column 64 c + 4 f + j with 64 c + 16 j + f = RR i + lr.
   const int lr = 8 * wave + (lane >> 3);
   const uint32_t lslot = 16u * (uint32_t)((lane & 7) ^ g_swz(lr));
   const uint32_t off_a = (uint32_t)lr * (uint32_t)k + lslot;
@@ -254,16 +259,18 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   const int kb = st0 * 128;
   auto issue = [&](int st, uint8_t* ab, uint8_t* bb) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < (NA > NB ? NA : NB); ++i) {
+      const int a_first = RR * i, b_first = (RR * i & ~63) + ((RR * i & 63) >> 4);
       const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(a_base + (int64_t)(64 * i) * k), (short)0, max(rows - 64 * i, 0) * k, 0x00020000);
+          (void*)(a_base + (int64_t)a_first * k), (short)0, max(rows - a_first, 0) * k, 0x00020000);
       const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(b_base + (int64_t)(64 * i) * k), (short)0, max(cols - 64 * i, 0) * k, 0x00020000);
+          (void*)(b_base + (int64_t)b_first * k), (short)0, max(cols - b_first, 0) * k, 0x00020000);
       if (i < NA)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (i8_lds_t)(ab + (8 * i + wave) * 1024), 16,
-                                                 off_a, kb + st * 128, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16,
-                                               off_b, kb + st * 128, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            a_rsrc, (i8_lds_t)(ab + (WAVES * i + wave) * 1024), 16, off_a, kb + st * 128, 0, 0);
+      if (i < NB)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            b_rsrc, (i8_lds_t)(bb + (WAVES * i + wave) * 1024), 16, off_b, kb + st * 128, 0, 0);
     }
   };
   issue(0, a0, b0);
@@ -276,7 +283,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     return at < B_STAGE ? b0 + at : at < 2 * B_STAGE ? b1 + (at - B_STAGE) : a0 + (at - 2 * B_STAGE);
   };
   auto fetch_t = [&]() {
-    for (int q = tid; q < BM * rank8; q += G_THREADS) {
+    for (int q = tid; q < BM * rank8; q += THREADS) {
       const int row = q % BM, r8 = q / BM;
       u32x4 part[3];
       project_sum8(t_part, m, rank, slices, (int)m0 + min(row, rows - 1), 8 * r8, part);
@@ -285,26 +292,33 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
         if (p < parts) *reinterpret_cast<u32x4*>(t_chunk(p, r8, row)) = part[p];
     }
   };
-  bf16x8 bu[FN];   // rows of up, eight ranks at a time
+  // rows of up, eight ranks per lane group.  The 32-wide MFMA takes rank 16
+  // twice: lane groups 0, 1 carry one part of t, groups 2, 3 the next.
+  const bool twice = rank8 == 2;
+  bf16x8 bu[FN];
   auto fetch_up = [&](int rr) {
+    const int r8 = twice ? g & 1 : rr + g;
 #pragma unroll
     for (int j = 0; j < FN; ++j)
-      bu[j] = rr + g < rank8 ? *reinterpret_cast<const bf16x8*>(
-                                   up + (brow0 + min(c0 + j, cols - 1)) * rank + 8 * (rr + g))
-                             : (bf16x8){};
+      bu[j] = r8 < rank8 ? *reinterpret_cast<const bf16x8*>(
+                               up + (brow0 + min(c0 + j, cols - 1)) * rank + 8 * r8)
+                         : (bf16x8){};
   };
   if constexpr (!SPLIT) {
     // what the epilogue needs comes in with the first stages
-    if (tid < BM)
-      row_s[tid] = xs[m0 + min(tid, rows - 1)];
-    else if (tid >= 256)
-      col_w[tid - 256] = fp16_bits_to_f32(scales[brow0 + min(tid - 256, cols - 1)]);
+    for (int i = tid; i < BM + BN; i += THREADS) {
+      if (i < BM)
+        row_s[i] = xs[m0 + min(i, rows - 1)];
+      else
+        col_w[i - BM] = fp16_bits_to_f32(scales[brow0 + min(i - BM, cols - 1)]);
+    }
     if (rank8 <= 2) fetch_t();
     fetch_up(0);
   }
 
-  // fragment addresses: K half h is chunks 4 h .. 4 h + 3
-  const uint32_t a_row = (uint32_t)(16 * FM * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
+  // fragment addresses: K half h is chunks 4 h .. 4 h + 3; 16-row tile i of
+  // wave row wm is tile 2 i + wm of the workgroup
+  const uint32_t a_row = (uint32_t)(16 * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
   uint32_t slot[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) slot[h] = 16u * (uint32_t)((4 * h + g) ^ g_swz(fr));
@@ -313,46 +327,6 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (i32x4){0, 0, 0, 0};
-  struct Frag {
-    i32x4 a[FM], b[FN];
-  };
-  auto read = [&](Frag& f, const uint8_t* ab, const uint8_t* bb, int h) {
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-      f.b[j] = *reinterpret_cast<const i32x4*>(bb + b_row + slot[h] + j * 2048);
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-      f.a[i] = *reinterpret_cast<const i32x4*>(ab + a_row + slot[h] + i * 2048);
-  };
-  auto compute = [&](const Frag& f) {
-#pragma unroll
-    for (int i = 0; i < FM; ++i)
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
-  };
-  auto interleave = [&]() {
-#pragma unroll
-    for (int i = 0; i < FM + FN; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // one LDS read
-      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 4 ? 2 : 1, 0);   // two MFMAs
-    }
-    __builtin_amdgcn_sched_group_barrier(0x008, FM >= 4 ? FM * FN - 2 * (FM + FN) : 1, 0);
-  };
-  auto interleave_loads = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // one global load
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 2 ? FM * FN / 8 : 1, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, FM >= 2 ? FM * FN / 8 : 1, 0);
-    }
-  };
   auto sync = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);
@@ -360,33 +334,85 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  // One stage.  The K half in registers is contracted while the next one is
-  // read.  At the barrier every wave has read all of the stage, so its buffers
-  // take stage st + 2, and stage st + 1 has landed.  Loads past the last stage
-  // fetch the last one again, into buffers that are not read any more.
-  Frag f0, f1;
-  auto stage = [&](int st, uint8_t* ab, uint8_t* bb, const uint8_t* an, const uint8_t* bn) {
-    read(f1, ab, bb, 1);
-    compute(f0);
-    interleave();
-    sync();
-    issue(min(st + 2, ST - 1), ab, bb);
-    read(f0, an, bn, 0);
-    compute(f1);
-    interleave_loads();
-    __builtin_amdgcn_sched_barrier(0);
-  };
   sync();
-  read(f0, a0, b0, 0);
-  for (int st = 0; st < ST; st += 2) {
-    stage(st, a0, b0, a1, b1);
-    stage(st + 1, a1, b1, a0, b0);
-  }
+  // the loop over the first F of the wave's FM row tiles
+  auto contract = [&](auto count) {
+    constexpr int F = decltype(count)::value;
+    struct Frag {
+      i32x4 a[F], b[FN];
+    };
+    auto read = [&](Frag& f, const uint8_t* ab, const uint8_t* bb, int h) {
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+        f.b[j] = *reinterpret_cast<const i32x4*>(bb + b_row + slot[h] + j * 2048);
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+        f.a[i] = *reinterpret_cast<const i32x4*>(ab + a_row + slot[h] + i * 4096);
+    };
+    auto compute = [&](const Frag& f) {
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+    };
+    auto interleave = [&]() {
+#pragma unroll
+      for (int i = 0; i < F + FN; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);                // one LDS read
+        __builtin_amdgcn_sched_group_barrier(0x008, F >= 4 ? 2 : 1, 0);   // MFMAs
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, F >= 4 ? F * FN - 2 * (F + FN) : 1, 0);
+    };
+    // global loads spread over the MFMAs: in a burst behind the barrier they
+    // hold up every wave's issue (16 us of 4480 x 16384 x 6144)
+    auto interleave_loads = [&]() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);   // one global load
+        __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, F >= 2 ? F * FN / 8 : 1, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, F >= 2 ? F * FN / 8 : 1, 0);
+      }
+    };
+    // One stage.  The K half in registers is contracted while the next one is
+    // read.  At the barrier every wave has read all of the stage, so its buffers
+    // take stage st + 2, and stage st + 1 has landed.  Loads past the last stage
+    // fetch the last one again, into buffers that are not read any more.
+    Frag f0, f1;
+    auto stage = [&](int st, uint8_t* ab, uint8_t* bb, const uint8_t* an, const uint8_t* bn) {
+      read(f1, ab, bb, 1);
+      compute(f0);
+      interleave();
+      sync();
+      issue(min(st + 2, ST - 1), ab, bb);
+      read(f0, an, bn, 0);
+      compute(f1);
+      interleave_loads();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    read(f0, a0, b0, 0);
+    for (int st = 0; st < ST; st += 2) {
+      stage(st, a0, b0, a1, b1);
+      stage(st + 1, a1, b1, a0, b0);
+    }
+  };
+  // a group's last tile is often half empty: it contracts half the row tiles
+  constexpr int HALF = (FM + 1) / 2;
+  if (FM >= 4 && rows <= 32 * HALF)
+    contract(std::integral_constant<int, HALF>{});
+  else
+    contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
   __builtin_amdgcn_sched_barrier(0);
 
-  // acc[i][j][v] is row 16 (FM wm + i) + 4 g + v, column 64 wn + 4 fr + j
-  const int rbase = 16 * FM * wm;
+  // acc[i][j][v] is row 32 i + 16 wm + 4 g + v, column 64 wn + 4 fr + j
+  const int rbase = 16 * wm;
   if constexpr (SPLIT) {
     // the splits' integer sums meet in k_w8a8_join
     int32_t* dst = partial + ((int64_t)split * m + m0) * n + n0 + c0;
@@ -394,7 +420,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     for (int i = 0; i < FM; ++i)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = rbase + 16 * i + 4 * g + v;
+        const int r = rbase + 32 * i + 4 * g + v;
         if (r >= rows) continue;
         const i32x4 o = {acc[i][0][v], acc[i][1][v], acc[i][2][v], acc[i][3][v]};
         if (left >= 4) {
@@ -416,22 +442,23 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   const f32x4 wsc = *reinterpret_cast<const f32x4*>(&col_w[c0]);
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const f32x4 sr = *reinterpret_cast<const f32x4*>(&row_s[rbase + 16 * i + 4 * g]);
+    const f32x4 sr = *reinterpret_cast<const f32x4*>(&row_s[rbase + 32 * i + 4 * g]);
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int v = 0; v < 4; ++v) out[i][j][v] = (float)acc[i][j][v] * wsc[j] * sr[v];
   }
-  // rank-r branch t up^T (rank 16: the upper half of the 32-wide step reads zeros)
+  // rank-r branch t up^T
   for (int rr = 0; rr < rank8; rr += 4) {
-    const bool rk = rr + g < rank8;
     if (rr > 0) fetch_up(rr);
-    for (int p = 0; p < parts; ++p) {
+    for (int p = 0; p < parts; p += twice ? 2 : 1) {
+      const int part = twice ? p + (g >> 1) : p, r8 = twice ? g & 1 : rr + g;
+      const bool live = part < parts && r8 < rank8;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const bf16x8 at = rk ? *reinterpret_cast<const bf16x8*>(
-                                   t_chunk(p, rr + g, rbase + 16 * i + fr))
-                             : (bf16x8){};
+        const bf16x8 at =
+            live ? *reinterpret_cast<const bf16x8*>(t_chunk(part, r8, rbase + 32 * i + fr))
+                 : (bf16x8){};
 #pragma unroll
         for (int j = 0; j < FN; ++j)
           out[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(at, bu[j], out[i][j], 0, 0, 0);
@@ -443,7 +470,7 @@ __global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
-      const int r = rbase + 16 * i + 4 * g + v;
+      const int r = rbase + 32 * i + 4 * g + v;
       if (r >= rows) continue;
       const f32x4 o = {out[i][0][v], out[i][1][v], out[i][2][v], out[i][3][v]};
       store4(y, (m0 + r) * n + n0 + c0, o, left, y_bf16);
@@ -694,14 +721,14 @@ constexpr SmallTile kSmall[] = {{1, 1, 7.8, 1.15, 2.2, 0.0, 0.1},
                                 {2, 4, 12.0, 3.0, 6.0, 0.3, 0.6},
                                 {4, 4, 11.6, 5.2, 8.8, 0.5, 2.1}};
 struct LargeTile {
-  int rows;
+  int rows, cols;
   double fixed, tile, stage;     // us, us per round, us per stage and round
   double join, bytes, parts;     // join: us, MB of partial sums per us, rounds of parts count more
 };
-constexpr LargeTile kLarge[] = {{64, 7.1, 4.5, 0.77, 6.3, 2.6, 1.4},
-                                {128, 8.2, 7.5, 0.9, 7.8, 1.6, 1.0},
-                                {224, 0.0, 19.3, 1.0, 0, 0, 0},
-                                {256, 0.0, 20.7, 1.07, 0, 0, 0}};
+constexpr LargeTile kLarge[] = {{64, 256, 7.1, 4.5, 0.77, 6.3, 2.6, 1.4},
+                                {128, 256, 8.2, 7.5, 0.9, 7.8, 1.6, 1.0},
+                                {224, 256, 0.0, 19.3, 1.0, 0, 0, 0},
+                                {256, 256, 0.0, 20.7, 1.07, 0, 0, 0}};
 
 void choose_tile(W8A8Plan& p) {
   const int64_t nb = p.k / 256;
@@ -726,7 +753,7 @@ void choose_tile(W8A8Plan& p) {
   }
   for (const LargeTile& t : kLarge) {
     const double tiles =
-        i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN) / 256.0;
+        i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + t.cols - 1) / t.cols) / 256.0;
     for (int s : {1, 2, 3, 4, 6, 8, 12}) {
       if (s > nb || (s > 1 && t.bytes == 0)) break;
       double rounds = p.groups > 1 ? std::max(1.0, tiles * s + 0.3) : std::ceil(tiles * s);
@@ -736,7 +763,7 @@ void choose_tile(W8A8Plan& p) {
       if (us < best) {
         best = us;
         p.tile_m = t.rows;
-        p.tile_n = G_BN;
+        p.tile_n = t.cols;
         p.splits = s;
       }
     }
@@ -828,7 +855,7 @@ hipError_t launch_w8a8(const W8A8Plan& p, const uint16_t* x, const int32_t* offs
   if (err != hipSuccess) return err;
   const int64_t tiles =
       i8_tile_bound(p.m, p.groups, p.tile_m) * ((p.n + p.tile_n - 1) / p.tile_n);
-  if (p.tile_n < G_BN) {
+  if (p.tile_n <= 64) {
     const size_t slds = (size_t)3 * (p.rank / 8) * p.tile_m * 16 +
                         (size_t)p.waves * (p.tile_m / 16) * (p.tile_n / 16) * 1024;
 #define SQ_W8A8_STREAM(MT, NT, U)                                                                 \
@@ -843,17 +870,18 @@ hipError_t launch_w8a8(const W8A8Plan& p, const uint16_t* x, const int32_t* offs
     return hipGetLastError();
   }
   int32_t* part = reinterpret_cast<int32_t*>(base + p.off_part);
-#define SQ_W8A8_GEMM(FM, SPLIT)                                                                    \
-  hipLaunchKernelGGL((k_w8a8_gemm<FM, SPLIT>), dim3((unsigned)(tiles * p.splits)), dim3(G_THREADS), 0,    \
-                     stream, xq, xs, t, codes, scales, up, offsets, p.groups, y, m, n, k, p.rank,  \
-                     p.slices, y_bf16, p.splits, part)
+#define SQ_W8A8_GEMM(FM, WN, SPLIT)                                                                \
+  hipLaunchKernelGGL((k_w8a8_gemm<FM, WN, SPLIT>), dim3((unsigned)(tiles * p.splits)),             \
+                     dim3(128 * WN), 0, stream, xq, xs, t, codes, scales, up, offsets, p.groups,   \
+                     y, m, n, k, p.rank, p.slices, y_bf16, p.splits, part)
   if (p.splits > 1) {
-    if (p.tile_m == 128) SQ_W8A8_GEMM(4, true);
-    else SQ_W8A8_GEMM(2, true);
-  } else if (p.tile_m == 256) SQ_W8A8_GEMM(8, false);
-  else if (p.tile_m == 224) SQ_W8A8_GEMM(7, false);
-  else if (p.tile_m == 128) SQ_W8A8_GEMM(4, false);
-  else SQ_W8A8_GEMM(2, false);
+    if (p.tile_m == 128) SQ_W8A8_GEMM(4, 4, true);
+    else SQ_W8A8_GEMM(2, 4, true);
+  } else if (p.tile_n == 128) SQ_W8A8_GEMM(4, 2, false);
+  else if (p.tile_m == 256) SQ_W8A8_GEMM(8, 4, false);
+  else if (p.tile_m == 224) SQ_W8A8_GEMM(7, 4, false);
+  else if (p.tile_m == 128) SQ_W8A8_GEMM(4, 4, false);
+  else SQ_W8A8_GEMM(2, 4, false);
 #undef SQ_W8A8_GEMM
   if (p.splits > 1) {
     if ((err = hipGetLastError()) != hipSuccess) return err;

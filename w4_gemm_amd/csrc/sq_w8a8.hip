@@ -159,11 +159,8 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 }
 
 // ---------------------------------------------------------------- contraction
-// BM x BN output tile per workgroup (BM = 32 FM, BN = 64 WN), 2 x WN waves of
-// 16 FM x 64 (FM x 4 MFMA tiles).  WN = 4: the operands are shared most.  WN = 2
-// (128 x 128): two workgroups per CU, so that one's loads, scales and stores
-// run under the other's MFMAs; with short K that outweighs the doubled operand
-// traffic.  One stage = 128 bytes of K of each operand row, two
+// BM x 256 output tile per workgroup (BM = 32 FM), 2 x 4 waves of 16 FM x 64
+// (FM x 4 MFMA tiles).  One stage = 128 bytes of K of each operand row, two
 // stages in LDS.  Both operands stream global -> LDS with direct 16-byte
 // buffer loads that cover whole 128-byte lines (64-byte halves of lines cost
 // 5 % of the 4480 x 16384 x 6144 contraction).  Chunk c of LDS row r sits at
@@ -171,6 +168,8 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 // LDS row 64 w + 16 j + f of the weight holds output column 64 w + 4 f + j, so
 // that a lane ends up with four consecutive columns and stores them as they
 // are.
+constexpr int G_BN = 256, G_THREADS = 512;
+
 // Swizzle of 128-byte rows.  A loop of nothing but the fragment reads runs
 // 1.9 times as long under c ^ (r & 7) ^ ((r >> 3) & 1), 3.7 times without any.
 __device__ __forceinline__ int g_swz(int r) { return r & 7; }
@@ -197,18 +196,18 @@ __device__ __forceinline__ void store4(void* __restrict__ y, int64_t at, f32x4 o
   }
 }
 
-template <int FM, int WN, bool SPLIT>
-__global__ void __launch_bounds__(128 * WN, 4 / WN) k_w8a8_gemm(
+template <int FM, bool SPLIT>
+__global__ void __launch_bounds__(G_THREADS, 1) k_w8a8_gemm(
     const int8_t* __restrict__ xq, const float* __restrict__ xs,
     const float* __restrict__ t_part, const int8_t* __restrict__ codes,
     const uint16_t* __restrict__ scales, const uint16_t* __restrict__ up,
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ y, int m, int n, int k,
     int rank, int slices, int y_bf16, int splits, int32_t* __restrict__ partial) {
   constexpr int FN = 4, BM = 32 * FM;
-  constexpr int WAVES = 2 * WN, THREADS = 64 * WAVES, BN = 64 * WN;
-  // one load instruction of every wave covers RR rows of 128 bytes
-  constexpr int RR = 8 * WAVES, NA = (BM + RR - 1) / RR, NB = BN / RR;
-  constexpr int A_STAGE = NA * RR * 128, B_STAGE = BN * 128;
+  constexpr int BN = G_BN, WN = 4, WAVES = 8, THREADS = G_THREADS;
+  // one load instruction of every wave covers 64 rows of 128 bytes
+  constexpr int NA = (BM + 63) / 64, NB = BN / 64;
+  constexpr int A_STAGE = NA * 64 * 128, B_STAGE = BN * 128;
   __shared__ __attribute__((aligned(16))) uint8_t a0[A_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b0[B_STAGE];
@@ -247,10 +246,9 @@ __global__ void __launch_bounds__(128 * WN, 4 / WN) k_w8a8_gemm(
   const int ST =
       2 * __builtin_amdgcn_readfirstlane((int)((int64_t)(split + 1) * (k >> 8) / splits)) - st0;
 
-  // loaders: instruction i of wave w fills LDS rows RR i + 8 w .. +8, through a
-  // descriptor of its own so that one offset serves all; rows past the tile lie
-  // beyond their descriptor and fetch nothing.  Weight row RR i + lr of the
-  // stage holds column 64 c + 4 f + j with 64 c + 16 j + f = RR i + lr.
+  // loaders: instruction i of wave w fills LDS rows 64 i + 8 w .. +8, through a
+  // descriptor of its own (64 rows each) so that one offset serves all; rows
+  // past the tile lie beyond their descriptor and fetch nothing
   const int lr = 8 * wave + (lane >> 3);
   const uint32_t lslot = 16u * (uint32_t)((lane & 7) ^ g_swz(lr));
   const uint32_t off_a = (uint32_t)lr * (uint32_t)k + lslot;
@@ -259,18 +257,16 @@ __global__ void __launch_bounds__(128 * WN, 4 / WN) k_w8a8_gemm(
   const int kb = st0 * 128;
   auto issue = [&](int st, uint8_t* ab, uint8_t* bb) {
 #pragma unroll
-    for (int i = 0; i < (NA > NB ? NA : NB); ++i) {
-      const int a_first = RR * i, b_first = (RR * i & ~63) + ((RR * i & 63) >> 4);
+    for (int i = 0; i < NB; ++i) {
       const __amdgpu_buffer_rsrc_t a_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(a_base + (int64_t)a_first * k), (short)0, max(rows - a_first, 0) * k, 0x00020000);
+          (void*)(a_base + (int64_t)(64 * i) * k), (short)0, max(rows - 64 * i, 0) * k, 0x00020000);
       const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(b_base + (int64_t)b_first * k), (short)0, max(cols - b_first, 0) * k, 0x00020000);
+          (void*)(b_base + (int64_t)(64 * i) * k), (short)0, max(cols - 64 * i, 0) * k, 0x00020000);
       if (i < NA)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
             a_rsrc, (i8_lds_t)(ab + (WAVES * i + wave) * 1024), 16, off_a, kb + st * 128, 0, 0);
-      if (i < NB)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            b_rsrc, (i8_lds_t)(bb + (WAVES * i + wave) * 1024), 16, off_b, kb + st * 128, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          b_rsrc, (i8_lds_t)(bb + (WAVES * i + wave) * 1024), 16, off_b, kb + st * 128, 0, 0);
     }
   };
   issue(0, a0, b0);
@@ -700,38 +696,43 @@ __global__ void __launch_bounds__(512) k_w8a8_stream(
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Tile of the contraction.  Each form's time (us) is modelled and the least
-// chosen; the constants are fitted to 6400 timed (M, N, K, groups) between
+// chosen; the constants are fitted to 4400 timed (M, N, K, groups) between
 // 1 x 64 x 256 and 16384 x 4096 x 4096 / 4480 x 16384 x 16384, over which the
-// choice takes 1.017 times the best form on average.  What decides:
+// choice takes 1.015 times the best form on average.  What decides:
 //   small tiles (waves split K, operands straight from memory): the time grows
 //     with the K steps of a wave and with the tiles per CU; 16 x 32 reads the
 //     codes once for up to 16 rows (1 x 16384 x 6144: 25 us against 34 us for
 //     a 64 x 256 tile with 4 splits) and 64 x 64 shares them among more rows
-//     (777 x 1003 x 2304: 22 against 27 us);
+//     (777 x 1003 x 2304: 21 against 26 us);
 //   large tiles (operands shared in LDS): whole rounds of 256 tiles, one stage
 //     of 128 K after another; few tiles split K so that every CU has one (48 x
 //     6144 x 16384: 38 us with 8 splits, 175 us with one), at the price of the
-//     partial sums' trip through memory.
+//     partial sums' trip through memory;
+//   none is faster than its codes arrive.
+// 128 x 128 tiles of four waves, two workgroups per CU, were the best form by
+// up to 10 % at a few shapes (1024 x 4096 x 8192) and by 0.3 % on average: not
+// kept.
 struct SmallTile {
   int mt, nt;
   double fixed, step, share, enough, tile;
 };
-constexpr SmallTile kSmall[] = {{1, 1, 7.8, 1.15, 2.2, 0.0, 0.1},
-                                {1, 2, 8.4, 1.7, 3.0, 0.0, 0.3},
-                                {2, 4, 12.0, 3.0, 6.0, 0.3, 0.6},
-                                {4, 4, 11.6, 5.2, 8.8, 0.5, 2.1}};
+constexpr SmallTile kSmall[] = {{1, 1, 8.2, 1.05, 2.15, 0.0, 0.1},
+                                {1, 2, 9.0, 1.5, 3.05, 0.0, 0.3},
+                                {2, 4, 9.8, 3.5, 5.7, 0.2, 0.6},
+                                {4, 4, 11.9, 4.9, 8.9, 0.55, 1.2}};
 struct LargeTile {
-  int rows, cols;
+  int rows;
   double fixed, tile, stage;     // us, us per round, us per stage and round
   double join, bytes, parts;     // join: us, MB of partial sums per us, rounds of parts count more
 };
-constexpr LargeTile kLarge[] = {{64, 256, 7.1, 4.5, 0.77, 6.3, 2.6, 1.4},
-                                {128, 256, 8.2, 7.5, 0.9, 7.8, 1.6, 1.0},
-                                {224, 256, 0.0, 19.3, 1.0, 0, 0, 0},
-                                {256, 256, 0.0, 20.7, 1.07, 0, 0, 0}};
+constexpr LargeTile kLarge[] = {{64, 7.9, 4.2, 0.75, 6.8, 3.4, 1.37},
+                                {128, 7.3, 5.6, 1.0, 7.7, 1.9, 1.0},
+                                {224, 0.0, 14.2, 1.06, 0, 0, 0},
+                                {256, 0.0, 14.3, 1.17, 0, 0, 0}};
 
 void choose_tile(W8A8Plan& p) {
   const int64_t nb = p.k / 256;
+  const double codes = (double)std::min<int64_t>(p.groups, p.m) * (double)p.n * (double)p.k / 5.6e6;
   double best = 1e30;
   p.splits = 1;
   for (const SmallTile& t : kSmall) {
@@ -742,8 +743,10 @@ void choose_tile(W8A8Plan& p) {
                          (double)((p.n + 16 * t.nt - 1) / (16 * t.nt)) / 256.0;
     const int64_t waves =
         tiles > 4 ? std::clamp<int64_t>(nb / 2, 1, 8) : std::min<int64_t>(nb, 8);
-    const double us = t.fixed + t.step * (double)((nb + waves - 1) / waves) +
-                      t.share * std::max(0.0, tiles - t.enough) * (double)nb / 8.0 + t.tile * tiles;
+    const double us = t.fixed + std::max(codes, t.step * (double)((nb + waves - 1) / waves) +
+                                                    t.share * std::max(0.0, tiles - t.enough) *
+                                                        (double)nb / 8.0 +
+                                                    t.tile * tiles);
     if (us < best) {
       best = us;
       p.tile_m = 16 * t.mt;
@@ -753,17 +756,17 @@ void choose_tile(W8A8Plan& p) {
   }
   for (const LargeTile& t : kLarge) {
     const double tiles =
-        i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + t.cols - 1) / t.cols) / 256.0;
+        i8_expected_tiles(p.m, p.groups, t.rows) * (double)((p.n + G_BN - 1) / G_BN) / 256.0;
     for (int s : {1, 2, 3, 4, 6, 8, 12}) {
       if (s > nb || (s > 1 && t.bytes == 0)) break;
       double rounds = p.groups > 1 ? std::max(1.0, tiles * s + 0.3) : std::ceil(tiles * s);
       if (s > 1) rounds *= t.parts;
-      double us = t.fixed + rounds * (t.tile + t.stage * (double)p.k / 128.0 / s);
+      double us = t.fixed + std::max(codes, rounds * (t.tile + t.stage * (double)p.k / 128.0 / s));
       if (s > 1) us += t.join + (double)p.m * (double)p.n * s * 4e-6 / t.bytes;
       if (us < best) {
         best = us;
         p.tile_m = t.rows;
-        p.tile_n = t.cols;
+        p.tile_n = G_BN;
         p.splits = s;
       }
     }
@@ -778,11 +781,12 @@ int64_t i8_tile_bound(int64_t m, int groups, int tile_m) {
   return groups <= 1 ? (m + tile_m - 1) / tile_m : (m + used * (tile_m - 1)) / tile_m;
 }
 
-// Row tiles to expect of them: groups end inside a tile.
+// Row tiles to expect: of exponentially distributed group sizes (experts are
+// loaded unevenly), the mean of ceil(size / tile_m) times the groups.
 double i8_expected_tiles(int64_t m, int groups, int tile_m) {
   if (groups <= 1) return (double)((m + tile_m - 1) / tile_m);
   const double used = (double)std::max<int64_t>(1, std::min<int64_t>(groups, m));
-  return used * std::max(1.0, (double)m / used / tile_m + 0.4);
+  return used / (1.0 - std::exp(-(double)tile_m * used / (double)std::max<int64_t>(m, 1)));
 }
 
 // Row tile and K slices of the rank-r projection: 32-row tiles from 64 rows per
@@ -870,18 +874,17 @@ hipError_t launch_w8a8(const W8A8Plan& p, const uint16_t* x, const int32_t* offs
     return hipGetLastError();
   }
   int32_t* part = reinterpret_cast<int32_t*>(base + p.off_part);
-#define SQ_W8A8_GEMM(FM, WN, SPLIT)                                                                \
-  hipLaunchKernelGGL((k_w8a8_gemm<FM, WN, SPLIT>), dim3((unsigned)(tiles * p.splits)),             \
-                     dim3(128 * WN), 0, stream, xq, xs, t, codes, scales, up, offsets, p.groups,   \
+#define SQ_W8A8_GEMM(FM, SPLIT)                                                                    \
+  hipLaunchKernelGGL((k_w8a8_gemm<FM, SPLIT>), dim3((unsigned)(tiles * p.splits)),                 \
+                     dim3(G_THREADS), 0, stream, xq, xs, t, codes, scales, up, offsets, p.groups,  \
                      y, m, n, k, p.rank, p.slices, y_bf16, p.splits, part)
   if (p.splits > 1) {
-    if (p.tile_m == 128) SQ_W8A8_GEMM(4, 4, true);
-    else SQ_W8A8_GEMM(2, 4, true);
-  } else if (p.tile_n == 128) SQ_W8A8_GEMM(4, 2, false);
-  else if (p.tile_m == 256) SQ_W8A8_GEMM(8, 4, false);
-  else if (p.tile_m == 224) SQ_W8A8_GEMM(7, 4, false);
-  else if (p.tile_m == 128) SQ_W8A8_GEMM(4, 4, false);
-  else SQ_W8A8_GEMM(2, 4, false);
+    if (p.tile_m == 128) SQ_W8A8_GEMM(4, true);
+    else SQ_W8A8_GEMM(2, true);
+  } else if (p.tile_m == 256) SQ_W8A8_GEMM(8, false);
+  else if (p.tile_m == 224) SQ_W8A8_GEMM(7, false);
+  else if (p.tile_m == 128) SQ_W8A8_GEMM(4, false);
+  else SQ_W8A8_GEMM(2, false);
 #undef SQ_W8A8_GEMM
   if (p.splits > 1) {
     if ((err = hipGetLastError()) != hipSuccess) return err;

@@ -107,6 +107,77 @@ def test_gradient_is_that_of_the_layer():
     assert float((y - ref).norm() / ref.norm()) < 2e-3
 
 
+# one shape for each tile form of the contractions (few rows and split K, 16 to 256 rows, tails cut
+# into parts), one layer and experts; odd widths where the form allows
+TILED_FWD = [
+    (4584, 781, 256, 1), (433, 5955, 256, 7), (3800, 17, 11776, 1), (1219, 55, 12800, 4),
+    (1, 10947, 1792, 1), (4, 4140, 512, 6), (1029, 7545, 256, 1), (659, 8211, 256, 4),
+    (3000, 4701, 256, 1), (608, 9170, 256, 4), (21, 4507, 2048, 1), (2502, 49, 1792, 2),
+    (65, 10276, 256, 1), (107, 4840, 256, 7), (17, 2381, 12544, 1), (26, 1519, 14592, 2),
+    (34, 10247, 1536, 1), (4869, 70, 1792, 9),
+]
+TILED_GRAD = [
+    (395, 1, 9728, 1), (107, 1, 13056, 5), (68, 4602, 11008, 1), (49, 8922, 15360, 2),
+    (1637, 1323, 5120, 1), (4657, 1329, 1792, 4), (1, 771, 256, 1), (1, 836, 256, 6),
+    (548, 2864, 14592, 1), (274, 3040, 14080, 9), (700, 2500, 1024, 1),
+]
+
+
+def _uneven(rng, m, groups):
+    share = rng.exponential(size=groups) + 0.05
+    return np.concatenate([[0], np.cumsum(rng.multinomial(m, share / share.sum()))])
+
+
+@pytest.mark.parametrize("m,n,k,groups", TILED_FWD)
+@pytest.mark.parametrize("rank,dt", [(0, F32), (16, BF16), (16, F32), (64, F32)])
+def test_forward_tiles(m, n, k, groups, rank, dt):
+    import w4_gemm_amd as W
+    rng = np.random.default_rng(m + n + k + rank)
+    x = R.make_rows(rng, m, k, dev())
+    if groups == 1:
+        lay = R.make_layer(rng, n, k, rank, dev())
+        R.check(_forward(x, lay, dt), *R.forward(x, *lay, dt))
+        return
+    lay = R.make_layer(rng, n, k, rank, dev(), groups=groups)
+    off = _uneven(rng, m, groups)
+    p = W.GroupedW8Payload(*lay)
+    out = torch.full((m, n), float("nan"), dtype=dt, device=dev())
+    W.grouped_fwd_w8a8(x, torch.from_numpy(off.astype(np.int32)).to(dev()), p, out=out,
+                       workspace=_workspace(W.grouped_fwd_w8a8_workspace_bytes(m, p)))
+    R.check(out, *_experts(R.forward, x, off, lay, dt, n))
+
+
+@pytest.mark.parametrize("m,n,k,groups", TILED_GRAD)
+@pytest.mark.parametrize("rank,dt", [(0, F32), (16, BF16), (16, F32), (64, F32)])
+def test_gradient_tiles(m, n, k, groups, rank, dt):
+    import w4_gemm_amd as W
+    rng = np.random.default_rng(m + n + k + rank)
+    dy = R.make_rows(rng, m, n, dev(), 1e-3)
+    if groups == 1:
+        lay = R.make_layer(rng, n, k, rank, dev())
+        R.check(_gradient(dy, lay, dt), *R.gradient(dy, *lay, dt))
+        return
+    lay = R.make_layer(rng, n, k, rank, dev(), groups=groups)
+    off = _uneven(rng, m, groups)
+    p = W.GroupedW8Payload(*lay)
+    out = torch.full((m, k), float("nan"), dtype=dt, device=dev())
+    W.grouped_dgrad_w8(dy, torch.from_numpy(off.astype(np.int32)).to(dev()), p, out=out,
+                       workspace=_workspace(W.grouped_dgrad_w8_workspace_bytes(m, p)))
+    R.check(out, *_experts(R.gradient, dy, off, lay, dt, k))
+
+
+def test_same_call_gives_the_same_bits():
+    """Forms that join split sums included: nothing depends on which workgroup ends first."""
+    rng = np.random.default_rng(9)
+    for m, n, k in ((17, 2381, 12544), (68, 4602, 11008), (300, 1000, 2048)):
+        lay = R.make_layer(rng, n, k, 32, dev())
+        x, dy = R.make_rows(rng, m, k, dev()), R.make_rows(rng, m, n, dev(), 1e-3)
+        y, dx = _forward(x, lay, F32), _gradient(dy, lay, F32)
+        for _ in range(3):
+            assert torch.equal(_forward(x, lay, F32), y)
+            assert torch.equal(_gradient(dy, lay, F32), dx)
+
+
 # ------------------------------------------------------------------ values
 def _value_rows(k):
     """Rows that go wrong first: zeros, one value, subnormals, the smallest and largest, wide
@@ -277,20 +348,27 @@ def test_experts_equal_single_layers():
 
 
 @pytest.mark.parametrize("bad", [[0, 50, 20, 60], [-5, 10, 30, 60], [0, 20, 90, 60], [60, 40, 20, 0],
-                                 [0, 2 ** 31 - 1, -2 ** 31, 60]])
-def test_offsets_that_are_wrong_stay_inside(bad):
-    """Offsets that are not ordered or not in range: rows may be wrong, nothing else is touched."""
+                                 [0, 2 ** 31 - 1, -2 ** 31, 60], [0, 600] * 10, [0, 600] * 40])
+@pytest.mark.parametrize("m,n,k", [(60, 70, 512), (600, 70, 512), (300, 2000, 4096)])
+def test_offsets_that_are_wrong_stay_inside(bad, m, n, k):
+    """Offsets that are not ordered or not in range, also many that claim the same rows: rows may be
+    wrong, nothing else is touched, neither behind the result nor behind the workspace."""
     import w4_gemm_amd as W
     rng = np.random.default_rng(22)
-    m, n, k = 60, 70, 512
-    p = W.GroupedW8Payload(*R.make_layer(rng, n, k, 16, dev(), groups=3))
+    if len(bad) > 20 and n > 100:
+        n = 300
+    p = W.GroupedW8Payload(*R.make_layer(rng, n, k, 16, dev(), groups=len(bad) - 1))
     offsets = torch.tensor(bad, dtype=torch.int32, device=dev())
     x, dy = R.make_rows(rng, m, k, dev()), R.make_rows(rng, m, n, dev())
-    for call, a, cols in ((W.grouped_fwd_w8a8, x, n), (W.grouped_dgrad_w8, dy, k)):
+    for call, size, a, cols in ((W.grouped_fwd_w8a8, W.grouped_fwd_w8a8_workspace_bytes, x, n),
+                                (W.grouped_dgrad_w8, W.grouped_dgrad_w8_workspace_bytes, dy, k)):
         whole = torch.full((m + 40, cols), 5.0, dtype=F32, device=dev())
-        call(a, offsets, p, out=whole[20:20 + m])
+        nbytes = size(m, p)
+        ws = torch.full((nbytes + (1 << 22),), 7, dtype=torch.uint8, device=dev())
+        call(a, offsets, p, out=whole[20:20 + m], workspace=ws[:nbytes])
         torch.cuda.synchronize()
         assert bool((whole[:20] == 5.0).all()) and bool((whole[m + 20:] == 5.0).all())
+        assert bool((ws[nbytes:] == 7).all())
 
 
 # ------------------------------------------------------------------ calls together

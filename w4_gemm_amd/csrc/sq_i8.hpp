@@ -37,9 +37,11 @@ __device__ __forceinline__ void group_range(const int32_t* __restrict__ offsets,
   }
 }
 
-// Number of tile_m-row tiles of all groups (offsets == null: one group of m rows).
+// Number of tile_m-row tiles of all groups (offsets == null: one group of m
+// rows), at most `most`: what nondecreasing offsets can need, and what the
+// launch and the partial sums' buffer are sized for.
 __device__ __forceinline__ int row_tile_count(const int32_t* __restrict__ offsets, int groups,
-                                              int m, int tile_m, int lane) {
+                                              int m, int tile_m, int most, int lane) {
   if (!offsets) return (m + tile_m - 1) / tile_m;
   int sum = 0;
   for (int e0 = 0; e0 < groups; e0 += 64) {
@@ -49,7 +51,7 @@ __device__ __forceinline__ int row_tile_count(const int32_t* __restrict__ offset
   }
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) sum += __shfl_xor(sum, s);
-  return __builtin_amdgcn_readfirstlane(sum);
+  return min(__builtin_amdgcn_readfirstlane(sum), most);
 }
 
 // Tile t in group order; false past the last one.  All 64 lanes take part.

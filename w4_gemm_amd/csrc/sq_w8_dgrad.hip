@@ -167,14 +167,15 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
     const int8_t* __restrict__ d, const float* __restrict__ ts, const float* __restrict__ t_part,
     const int8_t* __restrict__ codes, const uint16_t* __restrict__ down,
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ dx, int m, int n, int npad,
-    int k, int rank, int slices, int dx_bf16, int max_split, int64_t* __restrict__ partial) {
+    int k, int rank, int slices, int dx_bf16, int most_tiles, int max_split,
+    int64_t* __restrict__ partial) {
   constexpr int FN = 4, BM = 32 * FM;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int fr = lane & 15, g = lane >> 4;
   const int nt = k / D_BN;
-  const int mt = row_tile_count(offsets, groups, m, BM, lane);
+  const int mt = row_tile_count(offsets, groups, m, BM, most_tiles, lane);
   // workgroup b: tile b, or part (b - full) / rem of tile full + (b - full) % rem
   const int tiles = mt * nt;
   const Tail tail = tile_tail(tiles, max_split);
@@ -461,11 +462,11 @@ __global__ void __launch_bounds__(256) k_w8_dgrad_join(
     const int64_t* __restrict__ partial, const float* __restrict__ ts,
     const float* __restrict__ t_part, const uint16_t* __restrict__ down,
     const int32_t* __restrict__ offsets, int groups, void* __restrict__ dx, int m, int k, int rank,
-    int slices, int dx_bf16, int max_split, int tile_m) {
+    int slices, int dx_bf16, int max_split, int tile_m, int most_tiles) {
   __shared__ float t_lds[4][64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int nt = k >> 8, tiles = row_tile_count(offsets, groups, m, tile_m, lane) * nt;
+  const int nt = k >> 8, tiles = row_tile_count(offsets, groups, m, tile_m, most_tiles, lane) * nt;
   const Tail tail = tile_tail(tiles, max_split);
   const int splits = tail.splits, rem = tiles - tail.full;
   const int tail_tile = (int)blockIdx.x / (tile_m / 4);
@@ -641,14 +642,15 @@ hipError_t launch_w8_dgrad(const W8DgradPlan& p, const uint16_t* dy, const int32
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   // the tail's parts are at most one per CU more than the tiles
-  const int64_t bound = i8_tile_bound(p.m, p.groups, p.tile_m) * (p.k / D_BN);
+  const int most_tiles = (int)i8_tile_bound(p.m, p.groups, p.tile_m);
+  const int64_t bound = most_tiles * (p.k / D_BN);
   const int64_t tail_bound = std::min<int64_t>(bound, I8_CUS / 2);
   const int64_t tiles = p.max_split > 1 ? bound + std::min<int64_t>(bound * (p.max_split - 1), I8_CUS) : bound;
   int64_t* part = reinterpret_cast<int64_t*>(base + p.off_part);
 #define SQ_W8DG(FM)                                                                               \
   hipLaunchKernelGGL((k_w8_dgrad_gemm<FM>), dim3((unsigned)tiles), dim3(D_THREADS), 0, stream, d, \
                      ts, t, codes, down, offsets, p.groups, dx, m, n, npad, k, p.rank, p.slices,  \
-                     dx_bf16, p.max_split, part)
+                     dx_bf16, most_tiles, p.max_split, part)
   if (p.tile_m == 128) SQ_W8DG(4);
   else SQ_W8DG(2);
 #undef SQ_W8DG
@@ -656,7 +658,7 @@ hipError_t launch_w8_dgrad(const W8DgradPlan& p, const uint16_t* dy, const int32
   if (p.max_split > 1 && (p.groups > 1 || tile_tail((int)bound, p.max_split).splits > 1)) {
     hipLaunchKernelGGL(k_w8_dgrad_join, dim3((unsigned)(tail_bound * (p.tile_m / 4))), dim3(256), 0,
                        stream, part, ts, t, down, offsets, p.groups, dx, m, k, p.rank, p.slices,
-                       dx_bf16, p.max_split, p.tile_m);
+                       dx_bf16, p.max_split, p.tile_m, most_tiles);
     if ((err = hipGetLastError()) != hipSuccess) return err;
   }
   return hipSuccess;

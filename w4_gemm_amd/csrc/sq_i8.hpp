@@ -133,7 +133,7 @@ __device__ __forceinline__ u32x4 load8_u16(const uint16_t* __restrict__ p, int l
 // t_part[slice][row][r] = sum over the slice's columns of a[row][c] fac[c][r]
 // for the 16 RW rows of one tile: a bf16 [m][cols], fac bf16 [cols][rank] (the
 // group's factor), exact products and fp32 sums on bf16 MFMA.  The workgroup's
-// waves take the slice's 256-column blocks in turn and their sums are added in
+// waves take the slice's 64-column units (a line of a row) in turn and their sums are added in
 // wave order, so the result does not depend on timing.  Each wave stages 32
 // factor rows at a time in its own LDS (64 rank bytes) and reads them
 // transposed (eight consecutive c of one rank column per lane); the loads of
@@ -149,9 +149,9 @@ __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
   constexpr int RT = RANK / 16;
   const int tid = threadIdx.x, lane = tid & 63, fr = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
-  const int blocks = (cols + 255) >> 8;
-  const int b0 = (int)((int64_t)slice * blocks / slices);
-  const int b1 = (int)((int64_t)(slice + 1) * blocks / slices);
+  const int units = (cols + 63) >> 6;
+  const int b0 = (int)((int64_t)slice * units / slices);
+  const int b1 = (int)((int64_t)(slice + 1) * units / slices);
   uint8_t* stage = mem + wave * 64 * RANK;
   const uint16_t* arow[RW];   // rows past the tile repeat its last row
 #pragma unroll
@@ -160,9 +160,9 @@ __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
   struct Step {
     u32x4 a[RW], f[RT];
   };
-  const int steps = max(b1 - b0 - wave + waves - 1, 0) / waves * 8;   // 32 columns each
+  const int steps = max(b1 - b0 - wave + waves - 1, 0) / waves * 2;   // 32 columns each
   auto load = [&](Step& st, int q) {
-    const int c0 = (b0 + wave + waves * (q >> 3)) * 256 + 32 * (q & 7);
+    const int c0 = (b0 + wave + waves * (q >> 1)) * 64 + 32 * (q & 1);
     const int ca = c0 + 8 * g;
 #pragma unroll
     for (int i = 0; i < RW; ++i) {

@@ -242,6 +242,21 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
   const int tr_row = 16 * g + (fr >> 1);
   const uint32_t b_row = D_B + (uint32_t)tr_row * 256 + 8u * (uint32_t)(fr & 1);
   const int tr_swz = b_swz(tr_row);
+  // The epilogue's row scale and first ranks of t, where the registers allow:
+  // wave w ends up with rows 16 w + fr.  The 32-wide MFMA takes rank 16 twice:
+  // lane groups 0, 1 carry one part of t, groups 2, 3 the next.
+  constexpr bool EARLY = FM == 2;
+  const bool twice = rank == 16;
+  const uint16_t* down0 = down + ((int64_t)grp * k + k0) * rank;
+  float early_s = 0.0f;
+  u32x4 early_t[3] = {};
+  if (EARLY && 16 * wave < rows) {
+    const int er = (int)m0 + min(16 * wave + fr, rows - 1);
+    early_s = ts[er];
+    const int r0 = twice ? 8 * (g & 1) : 8 * g;
+    if (rank > 0) project_sum8(t_part, m, rank, slices, er, r0, early_t);
+  }
+
   i32x4 ah[FM][FN], al[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -394,20 +409,16 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
         w[i + h] = a - b;
       }
   const int row = 16 * wave + fr, rrow = (int)m0 + min(row, rows - 1);
-  const float f = ts[rrow] * 0.0625f;
+  const float f = (EARLY ? early_s : ts[rrow]) * 0.0625f;
 #pragma unroll
   for (int i = 0; i < 64; ++i) w[i] *= f;
   // rank-r branch with the columns as MFMA rows: output row 4g' + i of tile
   // (q, p) is column 64 q + 16 g' + 4 p + i, MFMA column fr the lane's row
-  const uint16_t* down0 = down + ((int64_t)grp * k + k0) * rank;
   const int dcol = 16 * (fr >> 2) + (fr & 3);
-  // the 32-wide MFMA takes rank 16 twice: lane groups 0, 1 carry one part of
-  // t, groups 2, 3 the next
-  const bool twice = rank == 16;
   for (int rr = 0; rr < rank; rr += 32) {
     const int r0 = twice ? 8 * (g & 1) : rr + 8 * g;
-    u32x4 part[3] = {};
-    project_sum8(t_part, m, rank, slices, rrow, r0, part);
+    u32x4 part[3] = {early_t[0], early_t[1], early_t[2]};
+    if (!EARLY || rr > 0) project_sum8(t_part, m, rank, slices, rrow, r0, part);
     if (twice && g >= 2) {
       part[0] = part[1];
       part[1] = (u32x4){0u, 0u, 0u, 0u};

@@ -371,6 +371,37 @@ def test_offsets_that_are_wrong_stay_inside(bad, m, n, k):
         assert bool((ws[nbytes:] == 7).all())
 
 
+def test_offsets_past_32_bits():
+    """Results, integers and stacked codes of more than 2^31 elements: the last rows and experts."""
+    import w4_gemm_amd as W
+    rng = np.random.default_rng(23)
+    m, n, k = 140_000, 16384, 256
+    lay = R.make_layer(rng, n, k, 16, dev())
+    x = torch.randn(m, k, device=dev()).bfloat16()
+    y = W.linear_fwd_w8a8(x, W.W8Payload(*lay), out_dtype=BF16)
+    for rows in (slice(0, 40), slice(131_050, 131_110), slice(m - 50, m)):
+        R.check(y[rows], *R.forward(x[rows], *lay, BF16))
+    del y
+    n, k = 48, 16384
+    lay = R.make_layer(rng, n, k, 16, dev())
+    dy = torch.randn(m, n, device=dev()).bfloat16()
+    dx = W.linear_dgrad_w8(dy, W.W8Payload(*lay), out_dtype=BF16)
+    for rows in (slice(0, 40), slice(131_050, 131_110), slice(m - 50, m)):
+        R.check(dx[rows], *R.gradient(dy[rows], *lay, BF16))
+    del dx
+    groups, n, k = 36, 8192, 8192
+    codes = torch.randint(-100, 101, (groups, n, k), dtype=torch.int8, device=dev())
+    w = torch.full((groups, n), 1e-4, dtype=torch.float16, device=dev())
+    p = W.GroupedW8Payload(codes, w, None, None)
+    off = np.concatenate([np.zeros(groups - 1), [30, 70]])     # the last two experts
+    offsets = torch.from_numpy(off.astype(np.int32)).to(dev())
+    x, dy = R.make_rows(rng, 70, k, dev()), R.make_rows(rng, 70, n, dev(), 1e-3)
+    y, dx = W.grouped_fwd_w8a8(x, offsets, p), W.grouped_dgrad_w8(dy, offsets, p)
+    for e, rows in ((groups - 2, slice(0, 30)), (groups - 1, slice(30, 70))):
+        R.check(y[rows], *R.forward(x[rows], codes[e], w[e], None, None, F32))
+        R.check(dx[rows], *R.gradient(dy[rows], codes[e], w[e], None, None, F32))
+
+
 # ------------------------------------------------------------------ calls together
 def test_layers_in_sequence_and_backward():
     """A two-layer expert block (up, down) with its backward, as a training step runs it."""

@@ -257,8 +257,9 @@ sq_status_t sq_linear_fwd_w8(const uint16_t *x, int64_t m, const sq_w8_t *p, voi
  *   q = round_half_even(fp32(r i)), |q| <= 127.
  * Every step is one correctly rounded operation, so q and s depend on the row
  * alone.  The integer sum is exact; the scales and the rank-r term (t = x @
- * lora_down summed in fp32, carried as bf16 hi + lo) are applied in fp32.  A
- * row of x that holds inf or NaN gives a row of NaN and touches no other row.
+ * lora_down summed in fp32, carried as a sum of two bf16 parts for bf16 results
+ * and three for fp32 ones) are applied in fp32.  A row of x that holds inf or
+ * NaN gives a row of NaN and touches no other row.
  * x bf16 [m][k], y fp32 or bf16 [m][n] (bf16 = RNE of the fp32 result).
  * K <= 65536 (SQ_E_SHAPE).  `workspace`: caller-owned device scratch of at
  * least sq_linear_fwd_w8a8_workspace_bytes(m, p) bytes (0 for unsupported
@@ -278,7 +279,8 @@ sq_status_t sq_linear_fwd_w8a8(const uint16_t *x, int64_t m, const sq_w8_t *p, v
  * that is a step of 2^-15 of the row's largest value.  d @ codes is exact in
  * integers; the rest is fp32.  A row that holds inf or NaN gives a row of NaN
  * and touches no other row.  dy bf16 [m][n], dx fp32 or bf16 [m][k].  Any
- * N <= 131072 (no multiple needed), K <= 65536.  Workspace and m == 0 as above. */
+ * N <= 131072 (no multiple needed), K <= 65536, m <= 2^25 (2^23 for N > 2048).
+ * Workspace and m == 0 as above. */
 size_t sq_linear_dgrad_w8_workspace_bytes(int64_t m, const sq_w8_t *p);
 sq_status_t sq_linear_dgrad_w8(const uint16_t *dy, int64_t m, const sq_w8_t *p, void *dx,
                                sq_dtype_t dx_dtype, void *workspace, size_t workspace_bytes,

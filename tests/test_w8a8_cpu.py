@@ -87,6 +87,17 @@ def test_workspace_bytes():
     assert _lib.sq_linear_fwd_w8a8_workspace_bytes(4, _payload(rank=24)) == 0
 
 
+def test_gradient_of_too_many_rows_is_refused():
+    """A gradient launch has fewer than 2^32 threads: 2^25 rows, 2^23 of more than 2048 values."""
+    for n, most in ((1, 1 << 25), (2048, 1 << 25), (2049, 1 << 23)):
+        p = _payload(n=n, k=256)
+        assert _lib.sq_linear_dgrad_w8_workspace_bytes(most, p) > 0
+        assert _lib.sq_linear_dgrad_w8_workspace_bytes(most + 1, p) == 0
+        assert _lib.sq_grouped_dgrad_w8_workspace_bytes(most + 1, 2, p) == 0
+        assert _lib.sq_linear_dgrad_w8(0x8000, most + 1, p, 0x9000, 0, 0xA000, 1 << 60, None) == 2
+        assert _lib.sq_linear_fwd_w8a8_workspace_bytes(most + 1, p) > 0
+
+
 def test_status_text_names_the_limits():
     assert "65536" in _lib.status_str(2) and "131072" in _lib.status_str(2)
 

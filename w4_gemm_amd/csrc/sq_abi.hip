@@ -102,7 +102,8 @@ const char* sq_status_str(sq_status_t s) {
     case SQ_E_NULL: return "a required pointer is NULL";
     case SQ_E_SHAPE:
       return "bad shape: need K % 256 == 0, K >= 256, N >= 1, M >= 0 (W4 input gradient: N % 64 == 0; "
-             "8-bit products: K <= 65536, M < 2^31, groups >= 1, input gradient N <= 131072)";
+             "8-bit products: K <= 65536, M < 2^31, groups >= 1, their input gradient N <= 131072, "
+             "M <= 2^25 (2^23 for N > 2048))";
     case SQ_E_GROUP: return "group must be 32 or 64";
     case SQ_E_RANK: return "rank must be 0, 32 or 64 (int8 mode: 0, 16, 32 or 64; reserved 0)";
     case SQ_E_ALIGN: return "every pointer must be 16-byte aligned";
@@ -338,7 +339,10 @@ constexpr int64_t kI8MaxK = 65536, kI8MaxN = 131072;
 
 static bool i8_shape_ok(int64_t m, int32_t groups, const sq_w8_t* p, bool dgrad) {
   if (m < 0 || m > INT32_MAX || groups < 1 || p->k > kI8MaxK || p->n > INT32_MAX) return false;
-  if (dgrad && p->n > kI8MaxN) return false;
+  // a gradient row takes a wave up to N = 2048 and a workgroup beyond; one launch has fewer
+  // than 2^32 threads
+  if (dgrad && (p->n > kI8MaxN || m > (p->n <= 2048 ? int64_t{1} << 25 : int64_t{1} << 23)))
+    return false;
   // offsets that are not ordered can name up to ceil(m / 16) tiles per group,
   // which the device counts in 32 bits
   if ((m + 15) / 16 > INT32_MAX / groups) return false;

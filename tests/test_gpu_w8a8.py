@@ -326,6 +326,26 @@ def test_experts(counts, rank, dt):
         R.check(out, *_experts(R.gradient, dy, off, lay, dt, k))
 
 
+@pytest.mark.parametrize("lo,hi", [(3, 50), (0, 512), (64, 400), (510, 512), (7, 7)])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_one_expert_with_some_of_the_rows(lo, hi, dt):
+    """The plan is made for 512 rows (the gradient's tiles cut in two parts); the offsets leave
+    fewer tiles, that are cut into more parts, or none."""
+    import w4_gemm_amd as W
+    rng = np.random.default_rng(31)
+    m, n, k = 512, 4096, 4096
+    lay = R.make_layer(rng, n, k, 16, dev(), groups=1)
+    p = W.GroupedW8Payload(*lay)
+    offsets = torch.tensor([lo, hi], dtype=torch.int32, device=dev())
+    for call, size, ref, cols, scale in (
+            (W.grouped_fwd_w8a8, W.grouped_fwd_w8a8_workspace_bytes, R.forward, n, 1.0),
+            (W.grouped_dgrad_w8, W.grouped_dgrad_w8_workspace_bytes, R.gradient, k, 1e-3)):
+        a = R.make_rows(rng, m, k if cols == n else n, dev(), scale)
+        out = torch.full((m, cols), -77.0, dtype=dt, device=dev())
+        call(a, offsets, p, out=out, workspace=_workspace(size(m, p)))
+        R.check(out, *_experts(ref, a, [lo, hi], lay, dt, cols))
+
+
 def test_experts_equal_single_layers():
     """Each expert's rows are the bits that the one-layer calls give (no factors: the number of
     slices of the rank-r sum may differ)."""

@@ -666,7 +666,8 @@ hipError_t launch_w8_dgrad(const W8DgradPlan& p, const uint16_t* dy, const int32
   else SQ_W8DG(2);
 #undef SQ_W8DG
   if ((err = hipGetLastError()) != hipSuccess) return err;
-  if (p.max_split > 1 && (p.groups > 1 || tile_tail((int)bound, p.max_split).splits > 1)) {
+  // offsets may leave any number of tiles, so only the plan tells whether a tail can be cut
+  if (p.max_split > 1) {
     hipLaunchKernelGGL(k_w8_dgrad_join, dim3((unsigned)(tail_bound * (p.tile_m / 4))), dim3(256), 0,
                        stream, part, ts, t, down, offsets, p.groups, dx, m, k, p.rank, p.slices,
                        dx_bf16, p.max_split, p.tile_m, most_tiles);

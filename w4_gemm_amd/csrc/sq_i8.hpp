@@ -249,21 +249,16 @@ __device__ __forceinline__ void project_tile(const uint16_t* __restrict__ a,
 }
 
 // Workgroup b of the projection: row tile b / slices, slice b % slices.
-template <int RW, bool VEC>
+template <int RANK, int RW, bool VEC>
 __device__ __forceinline__ void project(const uint16_t* __restrict__ a,
                                         const uint16_t* __restrict__ fac,
                                         const int32_t* __restrict__ offsets, int groups,
                                         float* __restrict__ t_part, uint8_t* mem, int m, int cols,
-                                        int rank, int b, int slices) {
+                                        int b, int slices) {
   RowTile rt;
   if (!find_row_tile(offsets, groups, m, 16 * RW, b / slices, threadIdx.x & 63, rt)) return;
-  const uint16_t* f = fac + (int64_t)rt.group * cols * rank;
-  if (rank == 16)
-    project_tile<16, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
-  else if (rank == 32)
-    project_tile<32, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
-  else
-    project_tile<64, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
+  const uint16_t* f = fac + (int64_t)rt.group * cols * RANK;
+  project_tile<RANK, RW, VEC>(a, f, t_part, mem, m, cols, rt, b % slices, slices);
 }
 
 // t of one row, eight rank columns from r0, summed over the slices in order

@@ -37,17 +37,20 @@ constexpr int DP_THREADS = 256;
 // lo 64], zero past n: one 128-byte line holds both halves of 64 values.
 // A thread keeps the first HELD groups of eight values of its row in registers
 // between the two passes (longer rows are read again).
-// VEC: n is a multiple of eight (rows are 16-byte aligned then).
-template <int RW, bool VEC, int WPR, int HELD>
+// VEC: n is a multiple of eight (rows are 16-byte aligned then).  RANK (16 also
+// where there are no factors): the projection's registers set how many waves a
+// SIMD holds, the rows' too: 8192 x 2816 takes 28 us at rank 16, 38 us in a
+// kernel that has rank 64 in it as well.
+template <int RANK, int RW, bool VEC, int WPR, int HELD>
 __global__ void __launch_bounds__(DP_THREADS) k_w8_dgrad_prep(
     const uint16_t* __restrict__ dy, const uint16_t* __restrict__ scales,
     const uint16_t* __restrict__ up, const int32_t* __restrict__ offsets, int groups,
     int8_t* __restrict__ d, float* __restrict__ ts, float* __restrict__ t_part, int m, int n,
-    int npad, int rank, int project_wgs, int slices) {
+    int npad, int project_wgs, int slices) {
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63;
   if ((int)blockIdx.x < project_wgs) {
-    project<RW, VEC>(dy, up, offsets, groups, t_part, dyn, m, n, rank, blockIdx.x, slices);
+    project<RANK, RW, VEC>(dy, up, offsets, groups, t_part, dyn, m, n, blockIdx.x, slices);
     return;
   }
   __shared__ uint32_t row_max[4];
@@ -632,22 +635,29 @@ hipError_t launch_w8_dgrad(const W8DgradPlan& p, const uint16_t* dy, const int32
   const int64_t qwgs = wpr == 1 ? (p.m + 3) / 4 : p.m;
   const int64_t twgs = i8_tile_bound(p.m, p.groups, p.t_rows) * p.slices;
   const size_t lds = (size_t)(DP_THREADS / 64) * 64 * p.rank;
-#define SQ_W8DP(RW, VEC, WPR, HELD)                                                              \
-  hipLaunchKernelGGL((k_w8_dgrad_prep<RW, VEC, WPR, HELD>), dim3((unsigned)(qwgs + twgs)),       \
+#define SQ_W8DP(RANK, RW, VEC, WPR, HELD)                                                        \
+  hipLaunchKernelGGL((k_w8_dgrad_prep<RANK, RW, VEC, WPR, HELD>), dim3((unsigned)(qwgs + twgs)), \
                      dim3(DP_THREADS), lds, stream, dy, scales, up, offsets, p.groups, d, ts, t, \
-                     m, n, npad, p.rank, (int)twgs, p.slices)
-#define SQ_W8DP_ROWS(RW)                                   \
-  do {                                                     \
-    if (n % 8 != 0 && wpr == 1) SQ_W8DP(RW, false, 1, 0);  \
-    else if (n % 8 != 0) SQ_W8DP(RW, false, 4, 0);         \
-    else if (n <= 512) SQ_W8DP(RW, true, 1, 1);            \
-    else if (n <= 2048) SQ_W8DP(RW, true, 1, 4);           \
-    else if (n <= 4096) SQ_W8DP(RW, true, 4, 2);           \
-    else if (n <= 8192) SQ_W8DP(RW, true, 4, 4);           \
-    else SQ_W8DP(RW, true, 4, 8);                          \
+                     m, n, npad, (int)twgs, p.slices)
+#define SQ_W8DP_ROWS(RANK, RW)                                  \
+  do {                                                          \
+    if (n % 8 != 0 && wpr == 1) SQ_W8DP(RANK, RW, false, 1, 0); \
+    else if (n % 8 != 0) SQ_W8DP(RANK, RW, false, 4, 0);        \
+    else if (n <= 512) SQ_W8DP(RANK, RW, true, 1, 1);           \
+    else if (n <= 2048) SQ_W8DP(RANK, RW, true, 1, 4);          \
+    else if (n <= 4096) SQ_W8DP(RANK, RW, true, 4, 2);          \
+    else if (n <= 8192) SQ_W8DP(RANK, RW, true, 4, 4);          \
+    else SQ_W8DP(RANK, RW, true, 4, 8);                         \
   } while (0)
-  if (p.t_rows == 16) SQ_W8DP_ROWS(1);
-  else SQ_W8DP_ROWS(2);
+#define SQ_W8DP_RANK(RANK)                   \
+  do {                                       \
+    if (p.t_rows == 16) SQ_W8DP_ROWS(RANK, 1); \
+    else SQ_W8DP_ROWS(RANK, 2);              \
+  } while (0)
+  if (p.rank <= 16) SQ_W8DP_RANK(16);
+  else if (p.rank == 32) SQ_W8DP_RANK(32);
+  else SQ_W8DP_RANK(64);
+#undef SQ_W8DP_RANK
 #undef SQ_W8DP_ROWS
 #undef SQ_W8DP
   hipError_t err = hipGetLastError();

@@ -76,7 +76,12 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
   const int tid = threadIdx.x, lane = tid & 63;
   if ((int)blockIdx.x < project_wgs) {
-    project<RW, true>(x, down, offsets, groups, t_part, dyn, m, k, rank, blockIdx.x, slices);
+    if (rank == 16)
+      project<16, RW, true>(x, down, offsets, groups, t_part, dyn, m, k, blockIdx.x, slices);
+    else if (rank == 32)
+      project<32, RW, true>(x, down, offsets, groups, t_part, dyn, m, k, blockIdx.x, slices);
+    else
+      project<64, RW, true>(x, down, offsets, groups, t_part, dyn, m, k, blockIdx.x, slices);
     return;
   }
   const int wg = (int)blockIdx.x - project_wgs;

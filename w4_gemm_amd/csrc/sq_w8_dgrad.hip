@@ -364,6 +364,22 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
       }
     return;
   }
+  // Rank-r branch: output row 4g' + i of tile qp = 4 q + p of its MFMAs is column
+  // 64 q + 16 g' + 4 p + i.  down's rows of the first 32 ranks come in under the
+  // exchange and the transform where the registers allow (1001 x 2051 x 4096,
+  // rank 64: 36 -> 32 us; with 128 rows they spill).
+  const int dcol = 16 * (fr >> 2) + (fr & 3);
+  const int trow = (int)m0 + min(16 * wave + fr, rows - 1);
+  auto rank0 = [&](int rr) { return twice ? 8 * (g & 1) : rr + 8 * g; };
+  auto down8 = [&](int qp, int rr) {
+    const uint16_t* base = down0 + (64 * (qp >> 2) + 4 * (qp & 3)) * rank;
+    return *reinterpret_cast<const u32x4*>(base + (uint32_t)(dcol * rank + rank0(rr)));
+  };
+  u32x4 dv[EARLY ? 16 : 1], part[3] = {early_t[0], early_t[1], early_t[2]};
+  if (EARLY && rank > 0 && 16 * wave < rows) {
+#pragma unroll
+    for (int qp = 0; qp < 16; ++qp) dv[qp] = down8(qp, 0);
+  }
   __syncthreads();   // every wave is done with the stage buffers
   // Sums in fp32.  Column bits: fr 0-3, j 4-5, wn 6-7.  The butterflies over j
   // run here, the others after the exchange.
@@ -411,17 +427,17 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
         w[i] = a + b;
         w[i + h] = a - b;
       }
-  const int row = 16 * wave + fr, rrow = (int)m0 + min(row, rows - 1);
-  const float f = (EARLY ? early_s : ts[rrow]) * 0.0625f;
+  const int row = 16 * wave + fr;
+  const float f = (EARLY ? early_s : ts[trow]) * 0.0625f;
 #pragma unroll
   for (int i = 0; i < 64; ++i) w[i] *= f;
-  // rank-r branch with the columns as MFMA rows: output row 4g' + i of tile
-  // (q, p) is column 64 q + 16 g' + 4 p + i, MFMA column fr the lane's row
-  const int dcol = 16 * (fr >> 2) + (fr & 3);
+  // rank-r branch with the columns as MFMA rows, MFMA column fr the lane's row
   for (int rr = 0; rr < rank; rr += 32) {
-    const int r0 = twice ? 8 * (g & 1) : rr + 8 * g;
-    u32x4 part[3] = {early_t[0], early_t[1], early_t[2]};
-    if (!EARLY || rr > 0) project_sum8(t_part, m, rank, slices, rrow, r0, part);
+    if (!EARLY || rr > 0) project_sum8(t_part, m, rank, slices, trow, rank0(rr), part);
+    if (EARLY && rr > 0) {
+#pragma unroll
+      for (int qp = 0; qp < 16; ++qp) dv[qp] = down8(qp, rr);
+    }
     if (twice && g >= 2) {
       part[0] = part[1];
       part[1] = (u32x4){0u, 0u, 0u, 0u};
@@ -429,21 +445,17 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
       part[1] = part[2];
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int qp = 0; qp < 16; ++qp) {
+      const bf16x8 dn = __builtin_bit_cast(bf16x8, EARLY ? dv[qp] : down8(qp, rr));
+      f32x4 acc = {w[4 * qp], w[4 * qp + 1], w[4 * qp + 2], w[4 * qp + 3]};
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dn, __builtin_bit_cast(bf16x8, part[0]), acc, 0, 0, 0);
+      if (!twice || !dx_bf16)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dn, __builtin_bit_cast(bf16x8, part[1]), acc, 0, 0, 0);
+      if (!twice && !dx_bf16)
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dn, __builtin_bit_cast(bf16x8, part[2]), acc, 0, 0, 0);
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const uint32_t at = (uint32_t)((64 * q + 4 * p + dcol) * rank + r0);
-        const bf16x8 dv = *reinterpret_cast<const bf16x8*>(down0 + at);
-        const int b = 16 * q + 4 * p;
-        f32x4 acc = {w[b], w[b + 1], w[b + 2], w[b + 3]};
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[0]), acc, 0, 0, 0);
-        if (!twice || !dx_bf16)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[1]), acc, 0, 0, 0);
-        if (!twice && !dx_bf16)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dv, __builtin_bit_cast(bf16x8, part[2]), acc, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[b + i] = acc[i];
-      }
+      for (int i = 0; i < 4; ++i) w[4 * qp + i] = acc[i];
+    }
   }
   if (row >= rows) return;
   const int64_t out0 = (m0 + row) * k + k0 + 16 * g;

@@ -119,7 +119,8 @@ TILED_FWD = [
 TILED_GRAD = [
     (395, 1, 9728, 1), (107, 1, 13056, 5), (68, 4602, 11008, 1), (49, 8922, 15360, 2),
     (1637, 1323, 5120, 1), (4657, 1329, 1792, 4), (1, 771, 256, 1), (1, 836, 256, 6),
-    (548, 2864, 14592, 1), (274, 3040, 14080, 9), (700, 2500, 1024, 1),
+    (548, 2864, 14592, 1), (274, 3040, 14080, 9), (700, 2500, 1024, 1), (3678, 2684, 2304, 1),
+    (4498, 4748, 2048, 4),
 ]
 
 

@@ -590,14 +590,15 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Rows of the tile and parts of a tail tile, by modelled time (us): rounds of a
 // fixed part and one part per stage, and for split tails the partial sums' trip
-// through memory.  Both sides measured: 512 x 4096 x 4096 42 us with 64 rows, 50
-// with 128; 4480 x 16384 x 6144 805 and 924; 1 x 16384 x 6144 34 us in 12 parts,
-// 163 whole; 2000 x 1000 x 8192 63 us, the same with its tail split.
+// through memory.  The constants are fitted to 9200 timed shapes, over which the
+// choice takes 1.009 times the best form.  Both sides measured: 512 x 4096 x 4096
+// 40 us with 64 rows, 51 with 128; 4480 x 16384 x 6144 866 and 751 (795 without
+// parts); 1 x 16384 x 6144 34 us in 8 parts, 107 whole; 2000 x 1000 x 8192 64 and 60.
 struct DgradTile {
   int rows;
   double tile, stage;   // us per round, us per stage of 64 and round
 };
-constexpr DgradTile kTiles[] = {{64, 9.0, 0.46}, {128, 12.0, 0.70}};
+constexpr DgradTile kTiles[] = {{64, 8.5, 0.46}, {128, 17.0, 0.67}};
 
 void choose_tile(W8DgradPlan& p) {
   const double stages = (double)p.npad / 64.0;
@@ -613,8 +614,8 @@ void choose_tile(W8DgradPlan& p) {
       double us = whole * (t.tile + stages * t.stage);
       if (rem > 0) us += t.tile + stages / parts * t.stage;
       // a launch and 16 bytes per partial sum
-      if (s > 1) us += 3.5;
-      if (parts > 1) us += 2.0 + rem * parts * std::min<double>(t.rows, rows_each) * 256 * 16 / 4.5e6;
+      if (s > 1) us += 3.8;
+      if (parts > 1) us += 4.3 + rem * parts * std::min<double>(t.rows, rows_each) * 256 * 16 / 3.9e6;
       if (us < best) {
         best = us;
         p.tile_m = t.rows;

@@ -335,7 +335,7 @@ sq_status_t sq_linear_fwd_w8(const uint16_t* x, int64_t m, const sq_w8_t* p, voi
 // ---------------------------------------------------------------- 8-bit products
 // Sizes that the 8-bit products take: a row of x on one workgroup (K <= 65536),
 // exact int32 sums, 32-bit row numbers and a launch of fewer than 2^31 workgroups.
-constexpr int64_t kI8MaxK = 65536, kI8MaxN = 131072;
+constexpr int64_t kI8MaxK = 65536, kI8MaxN = sq::I8_DGRAD_MAX_N;
 
 static bool i8_shape_ok(int64_t m, int32_t groups, const sq_w8_t* p, bool dgrad) {
   if (m < 0 || m > INT32_MAX || groups < 1 || p->k > kI8MaxK || p->n > INT32_MAX) return false;

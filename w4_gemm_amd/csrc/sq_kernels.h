@@ -109,6 +109,8 @@ hipError_t launch_dgrad(const DgradPlan& plan, const uint16_t* dy, const uint8_t
 
 // 8-bit products of the int8 mode.  offsets == null: one layer (groups = 1);
 // else rows offsets[e] .. offsets[e+1]-1 use expert e of stacked payloads.
+// N of the input gradient at most: its int32 sums are exact up to there.
+constexpr int64_t I8_DGRAD_MAX_N = 131072;
 int64_t i8_tile_bound(int64_t m, int groups, int tile_m);
 double i8_expected_tiles(int64_t m, int groups, int tile_m);
 void i8_project_plan(int64_t m, int groups, int64_t cols, int waves, int rank, int* t_rows,

@@ -11,8 +11,10 @@
 // value), and the product runs as two 8-bit ones on
 // v_mfma_i32_16x16x64_i8 that share each fragment of c: it costs what one
 // fp16 product costs and converts no codes.  The sums are exact in int32 for
-// N <= 131072.  A row that holds inf or NaN (or meets a scale that is) gives
-// a row of NaN.
+// N <= 131072: hi's stay below 127 * 128 * 131072 < 2^31, lo's reach
+// 128 * 128 * 131072 = 2^31 at that N alone, where the product mends the one
+// sum that wraps.  A row that holds inf or NaN (or meets a scale that is)
+// gives a row of NaN.
 //
 // Kernels:
 //   k_w8_dgrad_prep  hi, lo, t of every row, and the N slices of dy up
@@ -347,6 +349,21 @@ __global__ void __launch_bounds__(D_THREADS, 1) k_w8_dgrad_gemm(
     contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
   __builtin_amdgcn_sched_barrier(0);
+  // A low sum of 2^31 (every lo and every code -128: a row below the absmax
+  // floor) has wrapped to INT32_MIN, which no other sum gives, as none is below
+  // -127 * 128 * 131072.  256 of it move over to the high sum.
+  if (n == I8_DGRAD_MAX_N) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          if (al[i][j][v] == INT32_MIN) {
+            al[i][j][v] = INT32_MAX - 255;
+            ah[i][j][v] += 1;
+          }
+  }
 
   // lane (fr, g) holds rows 4g + v and column fr of each 16 x 16 tile
   if (splits > 1) {

@@ -138,6 +138,8 @@ def lib() -> ctypes.CDLL:
             f = getattr(L, name + "_workspace_bytes")
             f.argtypes = [i64, i32, P8]
             f.restype = ctypes.c_size_t
+        L.sqi_i8_form.argtypes = [i64, i32, P8, i32, ctypes.POINTER(i32)]
+        L.sqi_i8_form.restype = ctypes.c_int
         PX = ctypes.POINTER(SqMx4)
         L.sq_quantize_weight_mx4.argtypes = [vp, PX, vp, vp]
         L.sq_quantize_weight_mx4.restype = ctypes.c_int
@@ -269,6 +271,17 @@ def sq_grouped_dgrad_w8(dy, m: int, offsets, groups: int, p: SqW8, dx, dx_dtype:
                         workspace_bytes: int, stream) -> int:
     return (_lib or lib()).sq_grouped_dgrad_w8(dy, m, offsets, groups, p, dx, dx_dtype,
                                                workspace, workspace_bytes, stream)
+
+
+def i8_form(m: int, n: int, k: int, groups: int = 1, rank: int = 0, dgrad: bool = False) -> tuple:
+    """Form of the kernels that an 8-bit product of these sizes takes: tile rows, tile columns, K
+    splits (input gradient: parts of a tail tile at most), projection tile rows, projection slices."""
+    form = (ctypes.c_int32 * 5)()
+    p = SqW8(n, k, rank, 0, None, None, None, None)
+    status = lib().sqi_i8_form(m, groups, p, dgrad, form)
+    if status != SQ_OK:
+        raise ValueError(status_str(status))
+    return tuple(form)
 
 
 def sq_quantize_weight_mx4(w, p: SqMx4, dev_flags, stream) -> int:

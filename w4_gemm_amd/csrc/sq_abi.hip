@@ -430,6 +430,26 @@ sq_status_t sq_grouped_dgrad_w8(const uint16_t* dy, int64_t m, const int32_t* of
                     stream, true);
 }
 
+// Which form of the kernels a call takes, for callers that must know (the tests
+// of every form); not part of the ABI.  form: rows and columns of the product's
+// tile, K splits (forward) or parts of a tail tile at most (gradient), rows of a
+// projection tile, projection slices.  Sizes as the entry points check them.
+sq_status_t sqi_i8_form(int64_t m, int32_t groups, const sq_w8_t* p, int32_t dgrad,
+                        int32_t form[5]) {
+  if (!form) return SQ_E_NULL;
+  if (i8_workspace_bytes(m, groups, p, dgrad != 0) == 0) return SQ_E_SHAPE;
+  if (dgrad) {
+    const sq::W8DgradPlan plan = sq::plan_w8_dgrad(m, p->n, p->k, groups, p->rank);
+    const int32_t f[5] = {plan.tile_m, 256, plan.max_split, plan.t_rows, plan.slices};
+    memcpy(form, f, sizeof f);
+  } else {
+    const sq::W8A8Plan plan = sq::plan_w8a8(m, p->n, p->k, groups, p->rank);
+    const int32_t f[5] = {plan.tile_m, plan.tile_n, plan.splits, plan.t_rows, plan.slices};
+    memcpy(form, f, sizeof f);
+  }
+  return SQ_OK;
+}
+
 // ---------------------------------------------------------------- MXFP4 mode
 sq_status_t sq_quantize_weight_mx4(const float* w, const sq_mx4_t* p, int32_t* dev_flags,
                                    void* stream) {

@@ -1,4 +1,5 @@
 """The int8 mode's 8-bit products at the ends of their ranges, against the 64-bit reference."""
+import numpy as np
 import pytest
 import torch
 
@@ -43,3 +44,17 @@ def test_low_half_of_the_longest_gradient_rows(m, k):
                            out_dtype=F32)
     for block in dx.view(m, k // 256, 256).unbind(1):
         R.check(block, want[which], tol[which])
+
+
+@pytest.mark.parametrize("m", [1, 3, 70])
+@pytest.mark.parametrize("rank", [32, 64])
+@pytest.mark.parametrize("dt", [F32, BF16], ids=["f32", "bf16"])
+def test_longest_forward_rows_with_the_widest_factors(m, rank, dt):
+    """K = 65536: a pre-phase workgroup of 16 waves, whose projection takes 64 * rank bytes of LDS each,
+    16- and 32-row projection tiles."""
+    import w4_gemm_amd as W
+    rng = np.random.default_rng(m + rank)
+    n, k = 40, 65536
+    lay = R.make_layer(rng, n, k, rank, dev())
+    x = R.make_rows(rng, m, k, dev())
+    R.check(W.linear_fwd_w8a8(x, W.W8Payload(*lay), out_dtype=dt), *R.forward(x, *lay, dt))

@@ -7,8 +7,12 @@
 // of v = fp32(dy w) is held as 16-bit integers
 //   a = max(max_n |v|, 2^-100), t = fp32(a / 32512), i = fp32(32512 / a)
 //   d = round_half_even(fp32(v i)) = 256 hi + lo,   |hi| <= 127, -128 <= lo < 128
-// (a step of 2^-15 of the row's largest value, against fp16's 2^-11 of each
-// value), and the product runs as two 8-bit ones on
+// (a step of 2^-15 of the row's largest value: finer than fp16's 2^-11 of each
+// value down to 2^-4 of the largest, coarser below; relative error of dx over
+// 4096 x 1024, fp16 rows in brackets: Gaussian rows 3.5e-5 [2.1e-4], Student t
+// with 2 degrees of freedom 2.3e-4 [1.9e-4], one column x 1000 5.6e-4 [2.1e-5],
+// softmax minus one-hot 5.4e-4 [1.7e-5]; a bf16 W_hat or dx has 1.7e-3), and
+// the product runs as two 8-bit ones on
 // v_mfma_i32_16x16x64_i8 that share each fragment of c: it costs what one
 // fp16 product costs and converts no codes.  The sums are exact in int32 for
 // N <= 131072: hi's stay below 127 * 128 * 131072 < 2^31, lo's reach

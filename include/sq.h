@@ -302,7 +302,9 @@ sq_status_t sq_linear_dgrad_w8(const uint16_t *dy, int64_t m, const sq_w8_t *p, 
  * captured graph follows new contents.  An expert may have no rows.  Rows
  * before offsets[0] and from offsets[groups] on are left as they were.  Each
  * value is clamped into [0, m] on the device, so wrong offsets give wrong
- * rows but no access outside the tensors.  groups >= 1, m < 2^31. */
+ * rows but no access outside the tensors.  groups >= 1, m < 2^31 and
+ * ceil(m / 16) * groups < 2^31 (the device counts tiles in 32 bits); offsets
+ * is 16-byte aligned like every pointer. */
 size_t sq_grouped_fwd_w8a8_workspace_bytes(int64_t m, int32_t groups, const sq_w8_t *p);
 sq_status_t sq_grouped_fwd_w8a8(const uint16_t *x, int64_t m, const int32_t *offsets,
                                 int32_t groups, const sq_w8_t *p, void *y, sq_dtype_t y_dtype,

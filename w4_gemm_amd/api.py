@@ -431,7 +431,8 @@ def grouped_fwd_w8a8(x: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payload
                      out: torch.Tensor | None = None):
     """sq_grouped_fwd_w8a8: rows offsets[e]..offsets[e+1]-1 of x [M,K] through expert e.
 
-    offsets is an int32 device tensor [E+1]; rows outside the experts' ranges are left as they
+    offsets is an int32 device tensor [E+1], 16-byte aligned as all pointers are (a slice of a
+    longer tensor may not be: clone it); rows outside the experts' ranges are left as they
     were in `out` (undefined when it is allocated here)."""
     return _i8_product(_lib.sq_grouped_fwd_w8a8, _lib.sq_grouped_fwd_w8a8_workspace_bytes, x,
                        (p.k, p.n), p, offsets, out_dtype, workspace, out, "x")

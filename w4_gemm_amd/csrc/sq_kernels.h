@@ -133,7 +133,7 @@ hipError_t launch_w8a8(const W8A8Plan& plan, const uint16_t* x, const int32_t* o
                        hipStream_t stream);
 
 struct W8DgradPlan {
-  int64_t m, n, k, npad;       // npad: n rounded up to two stages of 128
+  int64_t m, n, k, npad;       // npad: n rounded up to 256, four stages of 64 rows
   int groups, rank;
   int t_rows, slices;          // row tile and N slices of the rank-r projection
   int tile_m, max_split;       // rows of the contraction tile; parts of a tail tile at most

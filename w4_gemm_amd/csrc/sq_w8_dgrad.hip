@@ -42,7 +42,8 @@ constexpr int DP_THREADS = 256;
 // others hold 4 / WPR rows each, WPR waves per row.  d is [m][npad / 64][hi 64 |
 // lo 64], zero past n: one 128-byte line holds both halves of 64 values.
 // A thread keeps the first HELD groups of eight values of its row in registers
-// between the two passes (longer rows are read again).
+// between the two passes (longer rows are read again, and so are rows whose
+// length is no multiple of eight, which keep none).
 // VEC: n is a multiple of eight (rows are 16-byte aligned then).  RANK (16 also
 // where there are no factors): the projection's registers set how many waves a
 // SIMD holds, the rows' too: 8192 x 2816 takes 28 us at rank 16, 38 us in a

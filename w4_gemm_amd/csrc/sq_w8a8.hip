@@ -172,7 +172,8 @@ __global__ void __launch_bounds__(1024) k_w8a8_prep(
 // slot c ^ g_swz(r).
 // LDS row 64 w + 16 j + f of the weight holds output column 64 w + 4 f + j, so
 // that a lane ends up with four consecutive columns and stores them as they
-// are.
+// are.  The 256-row tile (FM = 8, unsplit) takes all 256 registers and spills
+// seven of them (32 bytes of scratch per lane); no other form spills.
 constexpr int G_BN = 256, G_THREADS = 512;
 
 // Swizzle of 128-byte rows.  A loop of nothing but the fragment reads runs

@@ -237,6 +237,23 @@ class W8Payload:
                     _ptr(self.up), _ptr(self.down))
 
 
+def _one_layer(p):
+    """A stack of experts has the same C struct: a call for one layer would take the first one."""
+    if isinstance(p, GroupedW8Payload):
+        raise TypeError("this call takes the W8Payload of one layer; grouped_* take a stack")
+
+
+def _stack(p):
+    if not isinstance(p, GroupedW8Payload):
+        raise TypeError(f"grouped calls take a GroupedW8Payload, got {type(p).__name__}")
+
+
+def _stack_and_offsets(p, offsets):
+    _stack(p)
+    if offsets is None:
+        raise TypeError("grouped calls need the experts' row offsets")
+
+
 def empty_payload_w8(n: int, k: int, rank: int, device="cuda") -> W8Payload:
     up = torch.empty((n, rank), dtype=torch.bfloat16, device=device) if rank else None
     down = torch.empty((k, rank), dtype=torch.bfloat16, device=device) if rank else None
@@ -264,6 +281,7 @@ def quantize_weight_w8(w: torch.Tensor, up: torch.Tensor | None, down: torch.Ten
 
 def reconstruct_bf16_w8(p: W8Payload, out: torch.Tensor | None = None):
     """sq_reconstruct_bf16_w8: int8-mode payload -> bf16 W_hat [N,K]."""
+    _one_layer(p)
     if out is None:
         out = torch.empty((p.n, p.k), dtype=torch.bfloat16, device=p.codes.device)
     _require(out, torch.bfloat16, "out")
@@ -274,12 +292,14 @@ def reconstruct_bf16_w8(p: W8Payload, out: torch.Tensor | None = None):
 
 
 def fwd_w8_workspace_bytes(m: int, p: W8Payload) -> int:
+    _one_layer(p)
     return _lib.sq_linear_fwd_w8_workspace_bytes(m, p.abi())
 
 
 def linear_fwd_w8(x: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
                   workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """sq_linear_fwd_w8: bf16 x [M,K] -> y [M,N] (fp32 or bf16) for an int8-mode payload."""
+    _one_layer(p)
     _require(x, torch.bfloat16, "x")
     m = S.check_rows("x", x.shape, p.k)
     if out is None:
@@ -401,28 +421,33 @@ def _i8_product(call, sizes, a, into, p, offsets, out_dtype, workspace, out, in_
 
 
 def fwd_w8a8_workspace_bytes(m: int, p: W8Payload) -> int:
+    _one_layer(p)
     return _lib.sq_linear_fwd_w8a8_workspace_bytes(m, p.abi())
 
 
 def linear_fwd_w8a8(x: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """sq_linear_fwd_w8a8: bf16 x [M,K] -> y [M,N] (fp32 or bf16), 8-bit tokens and weights."""
+    _one_layer(p)
     return _i8_product(_lib.sq_linear_fwd_w8a8, _lib.sq_linear_fwd_w8a8_workspace_bytes, x,
                        (p.k, p.n), p, None, out_dtype, workspace, out, "x")
 
 
 def dgrad_w8_workspace_bytes(m: int, p: W8Payload) -> int:
+    _one_layer(p)
     return _lib.sq_linear_dgrad_w8_workspace_bytes(m, p.abi())
 
 
 def linear_dgrad_w8(dy: torch.Tensor, p: W8Payload, out_dtype=torch.float32,
                     workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
     """sq_linear_dgrad_w8: bf16 dy [M,N] -> dx = dy @ W_hat [M,K] (fp32 or bf16)."""
+    _one_layer(p)
     return _i8_product(_lib.sq_linear_dgrad_w8, _lib.sq_linear_dgrad_w8_workspace_bytes, dy,
                        (p.n, p.k), p, None, out_dtype, workspace, out, "dy")
 
 
 def grouped_fwd_w8a8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
+    _stack(p)
     return _lib.sq_grouped_fwd_w8a8_workspace_bytes(m, p.groups, p.abi())
 
 
@@ -434,11 +459,13 @@ def grouped_fwd_w8a8(x: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payload
     offsets is an int32 device tensor [E+1], 16-byte aligned as all pointers are (a slice of a
     longer tensor may not be: clone it); rows outside the experts' ranges are left as they
     were in `out` (undefined when it is allocated here)."""
+    _stack_and_offsets(p, offsets)
     return _i8_product(_lib.sq_grouped_fwd_w8a8, _lib.sq_grouped_fwd_w8a8_workspace_bytes, x,
                        (p.k, p.n), p, offsets, out_dtype, workspace, out, "x")
 
 
 def grouped_dgrad_w8_workspace_bytes(m: int, p: GroupedW8Payload) -> int:
+    _stack(p)
     return _lib.sq_grouped_dgrad_w8_workspace_bytes(m, p.groups, p.abi())
 
 
@@ -446,6 +473,7 @@ def grouped_dgrad_w8(dy: torch.Tensor, offsets: torch.Tensor, p: GroupedW8Payloa
                      out_dtype=torch.float32, workspace: torch.Tensor | None = None,
                      out: torch.Tensor | None = None):
     """sq_grouped_dgrad_w8: the input gradient of grouped_fwd_w8a8, rows and offsets alike."""
+    _stack_and_offsets(p, offsets)
     return _i8_product(_lib.sq_grouped_dgrad_w8, _lib.sq_grouped_dgrad_w8_workspace_bytes, dy,
                        (p.n, p.k), p, offsets, out_dtype, workspace, out, "dy")
 

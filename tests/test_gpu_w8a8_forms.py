@@ -209,3 +209,46 @@ def test_rows_that_are_not_finite_with_factors(rank, dgrad, dt):
             keep[m - 1] = False                   # a value that may overflow on the way
         if bool(keep.any()):
             R.check(got[keep], *ref(a[keep], *lay, dt))
+
+
+# ------------------------------------------------------------------ captured
+@pytest.mark.parametrize("dgrad,shape", WRONG, ids=[f"{'grad' if d else 'fwd'}-{s}" for d, s in WRONG])
+def test_split_plan_in_a_graph(dgrad, shape):
+    """A captured call whose sums are joined follows new rows and new offsets, which leave other
+    numbers of tiles and parts each time, eager calls with another workspace between the replays."""
+    import w4_gemm_amd as W
+    m, n, k, groups = shape
+    assert F.form(m, n, k, groups, 16, dgrad)[-1]
+    rng = np.random.default_rng(m + groups + 2)
+    call, size, ref, scale = _sides()[dgrad]
+    lay = R.make_layer(rng, n, k, 16, dev(), groups=groups)
+    p = W.GroupedW8Payload(*lay)
+    a = _rows(rng, m, n, k, dgrad, scale)
+    offsets = torch.zeros(groups + 1, dtype=torch.int32, device=dev())
+    out = torch.empty((m, k if dgrad else n), dtype=F32, device=dev())
+    ws = torch.full((size(m, p),), 255, dtype=torch.uint8, device=dev())
+    call(a, offsets, p, out=out, workspace=ws)           # loads the kernels
+    torch.cuda.synchronize()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(g, stream=side):
+            call(a, offsets, p, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    for rows in (m, max(1, m // 9), 0, m - 1, m // 2):
+        share = rng.exponential(size=groups) + 0.05
+        off = np.concatenate([[0], np.cumsum(rng.multinomial(rows, share / share.sum()))])
+        offsets.copy_(torch.from_numpy(off.astype(np.int32)))
+        a.copy_(_rows(rng, m, n, k, dgrad, scale))
+        out.fill_(-77.0)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        eager = torch.full_like(out, -77.0)
+        call(a, offsets, p, out=eager)
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager), rows
+        e = int(np.argmax(np.diff(off)))                 # the fullest expert against 64 bits
+        lo, hi = off[e], off[e + 1]
+        if hi > lo:
+            R.check(out[lo:hi], *ref(a[lo:hi], *(t[e] for t in lay), F32))
+        assert bool((out[rows:] == -77.0).all())

@@ -11,6 +11,9 @@ Entry points (C ABI in include/sq.h, same names here):
   sq_grouped_fwd_w8a8, sq_grouped_dgrad_w8 the same over several experts' payloads
   *_mx4                the MXFP4 mode (E2M1 codes, E8M0 block-32 exponents; the forward
                        quantizes the rotated activations too and runs on FP4 MFMA)
+  *_f8                 the 8-bit float mode (E4M3 codes, a power of two per block of 128, no
+                       rotation): quantizer, forward and input gradient, and sq_gated_fwd_f8,
+                       sq_gated_bwd_f8 for the gated half of an MLP; sq_grouped_* over experts
 The rank-32 SVD split that feeds the quantizer is a host step (svd_init).
 """
 from .api import (W4Payload, dgrad_workspace_bytes, empty_payload, fwd_workspace_bytes,
@@ -22,7 +25,14 @@ from .api import (W4Payload, dgrad_workspace_bytes, empty_payload, fwd_workspace
                   fwd_w8a8_workspace_bytes, linear_fwd_w8a8, dgrad_w8_workspace_bytes,
                   linear_dgrad_w8, GroupedW8Payload, stack_payloads_w8,
                   grouped_fwd_w8a8_workspace_bytes, grouped_fwd_w8a8,
-                  grouped_dgrad_w8_workspace_bytes, grouped_dgrad_w8)
+                  grouped_dgrad_w8_workspace_bytes, grouped_dgrad_w8,
+                  F8Payload, GroupedF8Payload, empty_payload_f8, quantize_weight_f8,
+                  stack_payloads_f8, fwd_f8_workspace_bytes, linear_fwd_f8,
+                  dgrad_f8_workspace_bytes, linear_dgrad_f8, grouped_fwd_f8_workspace_bytes,
+                  grouped_fwd_f8, grouped_dgrad_f8_workspace_bytes, grouped_dgrad_f8,
+                  gated_fwd_f8_workspace_bytes, gated_fwd_f8, gated_bwd_f8_workspace_bytes,
+                  gated_bwd_f8, grouped_gated_fwd_f8_workspace_bytes, grouped_gated_fwd_f8,
+                  grouped_gated_bwd_f8_workspace_bytes, grouped_gated_bwd_f8)
 from ._lib import SqError, abi_version
 from .svd_init import svd_init
 
@@ -37,4 +47,11 @@ __all__ = ["W4Payload", "empty_payload", "fwd_workspace_bytes", "linear_fwd", "l
            "fwd_w8a8_workspace_bytes", "linear_fwd_w8a8", "dgrad_w8_workspace_bytes",
            "linear_dgrad_w8", "GroupedW8Payload", "stack_payloads_w8",
            "grouped_fwd_w8a8_workspace_bytes", "grouped_fwd_w8a8",
-           "grouped_dgrad_w8_workspace_bytes", "grouped_dgrad_w8"]
+           "grouped_dgrad_w8_workspace_bytes", "grouped_dgrad_w8",
+           "F8Payload", "GroupedF8Payload", "empty_payload_f8", "quantize_weight_f8",
+           "stack_payloads_f8", "fwd_f8_workspace_bytes", "linear_fwd_f8",
+           "dgrad_f8_workspace_bytes", "linear_dgrad_f8", "grouped_fwd_f8_workspace_bytes",
+           "grouped_fwd_f8", "grouped_dgrad_f8_workspace_bytes", "grouped_dgrad_f8",
+           "gated_fwd_f8_workspace_bytes", "gated_fwd_f8", "gated_bwd_f8_workspace_bytes",
+           "gated_bwd_f8", "grouped_gated_fwd_f8_workspace_bytes", "grouped_gated_fwd_f8",
+           "grouped_gated_bwd_f8_workspace_bytes", "grouped_gated_bwd_f8"]

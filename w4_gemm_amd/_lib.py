@@ -16,7 +16,9 @@ SQ_F32, SQ_BF16 = 0, 1
 SQ_FLAG_NONFINITE, SQ_FLAG_SCALE_OVERFLOW, SQ_FLAG_FP16_RANGE = 1, 2, 4
 STATUS_NAMES = {0: "SQ_OK", 1: "SQ_E_NULL", 2: "SQ_E_SHAPE", 3: "SQ_E_GROUP", 4: "SQ_E_RANK",
                 5: "SQ_E_ALIGN", 6: "SQ_E_WORKSPACE", 7: "SQ_E_DTYPE", 8: "SQ_E_ARCH",
-                9: "SQ_E_HIP"}
+                9: "SQ_E_HIP", 10: "SQ_E_ACT"}
+SQ_ACT = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+SQ_F8_MAX = 1 << 20
 
 # every symbol include/sq.h declares
 EXPORTS = ("sq_quantize_weight", "sq_linear_fwd_workspace_bytes", "sq_linear_fwd",
@@ -29,7 +31,15 @@ EXPORTS = ("sq_quantize_weight", "sq_linear_fwd_workspace_bytes", "sq_linear_fwd
            "sq_linear_fwd_w8a8_workspace_bytes", "sq_linear_fwd_w8a8",
            "sq_linear_dgrad_w8_workspace_bytes", "sq_linear_dgrad_w8",
            "sq_grouped_fwd_w8a8_workspace_bytes", "sq_grouped_fwd_w8a8",
-           "sq_grouped_dgrad_w8_workspace_bytes", "sq_grouped_dgrad_w8")
+           "sq_grouped_dgrad_w8_workspace_bytes", "sq_grouped_dgrad_w8",
+           "sq_quantize_weight_f8", "sq_linear_fwd_f8_workspace_bytes", "sq_linear_fwd_f8",
+           "sq_linear_dgrad_f8_workspace_bytes", "sq_linear_dgrad_f8",
+           "sq_gated_fwd_f8_workspace_bytes", "sq_gated_fwd_f8",
+           "sq_gated_bwd_f8_workspace_bytes", "sq_gated_bwd_f8",
+           "sq_grouped_fwd_f8_workspace_bytes", "sq_grouped_fwd_f8",
+           "sq_grouped_dgrad_f8_workspace_bytes", "sq_grouped_dgrad_f8",
+           "sq_grouped_gated_fwd_f8_workspace_bytes", "sq_grouped_gated_fwd_f8",
+           "sq_grouped_gated_bwd_f8_workspace_bytes", "sq_grouped_gated_bwd_f8")
 SQ_FWD_STATIC_SCRATCH_BYTES = 64 << 20
 
 
@@ -72,6 +82,16 @@ class SqMx4(ctypes.Structure):
         ("exps", ctypes.c_void_p),
         ("lora_up", ctypes.c_void_p),
         ("lora_down", ctypes.c_void_p),
+    ]
+
+
+class SqF8(ctypes.Structure):
+    """Mirror of sq_f8_t (8-bit float mode)."""
+    _fields_ = [
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("exps", ctypes.c_void_p),
     ]
 
 
@@ -151,6 +171,22 @@ def lib() -> ctypes.CDLL:
         L.sq_linear_fwd_mx4_workspace_bytes.restype = ctypes.c_size_t
         L.sq_linear_fwd_mx4.argtypes = [vp, i64, PX, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
         L.sq_linear_fwd_mx4.restype = ctypes.c_int
+        PF, ci, sz = ctypes.POINTER(SqF8), ctypes.c_int, ctypes.c_size_t
+        L.sq_quantize_weight_f8.argtypes = [vp, ci, PF, vp, vp]
+        L.sq_quantize_weight_f8.restype = ci
+        for grouped, offs in (("", []), ("grouped_", [vp, i32])):
+            plain = grouped or "linear_"
+            for name, args in ((f"sq_{plain}fwd_f8", [vp, i64, *offs, PF, vp, ci]),
+                               (f"sq_{plain}dgrad_f8", [vp, i64, *offs, PF, vp, ci]),
+                               (f"sq_{grouped}gated_fwd_f8", [vp, i64, *offs, PF, PF, ci, vp, ci, vp, vp]),
+                               (f"sq_{grouped}gated_bwd_f8",
+                                [vp, vp, vp, i64, *offs, PF, PF, ci, vp, ci, vp, vp])):
+                f = getattr(L, name)
+                f.argtypes = [*args, vp, sz, vp]
+                f.restype = ci
+                f = getattr(L, name + "_workspace_bytes")
+                f.argtypes = [i64, *offs[1:], PF]
+                f.restype = sz
         L.sq_status_str.argtypes = [ctypes.c_int]
         L.sq_status_str.restype = ctypes.c_char_p
         L.sq_abi_version.argtypes = []
@@ -304,3 +340,88 @@ def sq_linear_fwd_mx4(x, m: int, p: SqMx4, y, y_dtype: int, workspace, workspace
                       stream) -> int:
     return lib().sq_linear_fwd_mx4(x, m, ctypes.byref(p), y, y_dtype, workspace, workspace_bytes,
                                    stream)
+
+
+def sq_quantize_weight_f8(w, w_dtype: int, p: SqF8, dev_flags, stream) -> int:
+    return lib().sq_quantize_weight_f8(w, w_dtype, p, dev_flags, stream)
+
+
+def sq_linear_fwd_f8_workspace_bytes(m: int, p: SqF8) -> int:
+    return (_lib or lib()).sq_linear_fwd_f8_workspace_bytes(m, p)
+
+
+def sq_linear_fwd_f8(x, m: int, p: SqF8, y, y_dtype: int, workspace, workspace_bytes: int,
+                     stream) -> int:
+    return (_lib or lib()).sq_linear_fwd_f8(x, m, p, y, y_dtype, workspace, workspace_bytes, stream)
+
+
+def sq_linear_dgrad_f8_workspace_bytes(m: int, p: SqF8) -> int:
+    return (_lib or lib()).sq_linear_dgrad_f8_workspace_bytes(m, p)
+
+
+def sq_linear_dgrad_f8(dy, m: int, p: SqF8, dx, dx_dtype: int, workspace, workspace_bytes: int,
+                       stream) -> int:
+    return (_lib or lib()).sq_linear_dgrad_f8(dy, m, p, dx, dx_dtype, workspace, workspace_bytes,
+                                              stream)
+
+
+def sq_grouped_fwd_f8_workspace_bytes(m: int, groups: int, p: SqF8) -> int:
+    return (_lib or lib()).sq_grouped_fwd_f8_workspace_bytes(m, groups, p)
+
+
+def sq_grouped_fwd_f8(x, m: int, offsets, groups: int, p: SqF8, y, y_dtype: int, workspace,
+                      workspace_bytes: int, stream) -> int:
+    return (_lib or lib()).sq_grouped_fwd_f8(x, m, offsets, groups, p, y, y_dtype, workspace,
+                                             workspace_bytes, stream)
+
+
+def sq_grouped_dgrad_f8_workspace_bytes(m: int, groups: int, p: SqF8) -> int:
+    return (_lib or lib()).sq_grouped_dgrad_f8_workspace_bytes(m, groups, p)
+
+
+def sq_grouped_dgrad_f8(dy, m: int, offsets, groups: int, p: SqF8, dx, dx_dtype: int, workspace,
+                        workspace_bytes: int, stream) -> int:
+    return (_lib or lib()).sq_grouped_dgrad_f8(dy, m, offsets, groups, p, dx, dx_dtype, workspace,
+                                               workspace_bytes, stream)
+
+
+def sq_gated_fwd_f8_workspace_bytes(m: int, gate: SqF8) -> int:
+    return (_lib or lib()).sq_gated_fwd_f8_workspace_bytes(m, gate)
+
+
+def sq_gated_fwd_f8(x, m: int, gate: SqF8, up: SqF8, act: int, h, h_dtype: int, g, u, workspace,
+                    workspace_bytes: int, stream) -> int:
+    return (_lib or lib()).sq_gated_fwd_f8(x, m, gate, up, act, h, h_dtype, g, u, workspace,
+                                           workspace_bytes, stream)
+
+
+def sq_gated_bwd_f8_workspace_bytes(m: int, gate: SqF8) -> int:
+    return (_lib or lib()).sq_gated_bwd_f8_workspace_bytes(m, gate)
+
+
+def sq_gated_bwd_f8(dh, g, u, m: int, gate: SqF8, up: SqF8, act: int, dx, dx_dtype: int, dg, du,
+                    workspace, workspace_bytes: int, stream) -> int:
+    return (_lib or lib()).sq_gated_bwd_f8(dh, g, u, m, gate, up, act, dx, dx_dtype, dg, du,
+                                           workspace, workspace_bytes, stream)
+
+
+def sq_grouped_gated_fwd_f8_workspace_bytes(m: int, groups: int, gate: SqF8) -> int:
+    return (_lib or lib()).sq_grouped_gated_fwd_f8_workspace_bytes(m, groups, gate)
+
+
+def sq_grouped_gated_fwd_f8(x, m: int, offsets, groups: int, gate: SqF8, up: SqF8, act: int, h,
+                            h_dtype: int, g, u, workspace, workspace_bytes: int, stream) -> int:
+    return (_lib or lib()).sq_grouped_gated_fwd_f8(x, m, offsets, groups, gate, up, act, h, h_dtype,
+                                                   g, u, workspace, workspace_bytes, stream)
+
+
+def sq_grouped_gated_bwd_f8_workspace_bytes(m: int, groups: int, gate: SqF8) -> int:
+    return (_lib or lib()).sq_grouped_gated_bwd_f8_workspace_bytes(m, groups, gate)
+
+
+def sq_grouped_gated_bwd_f8(dh, g, u, m: int, offsets, groups: int, gate: SqF8, up: SqF8, act: int,
+                            dx, dx_dtype: int, dg, du, workspace, workspace_bytes: int,
+                            stream) -> int:
+    return (_lib or lib()).sq_grouped_gated_bwd_f8(dh, g, u, m, offsets, groups, gate, up, act, dx,
+                                                   dx_dtype, dg, du, workspace, workspace_bytes,
+                                                   stream)

@@ -12,7 +12,7 @@ import torch
 
 from . import _lib
 from . import shapes as S
-from ._lib import SqError, SqMx4, SqW4, SqW8, SQ_BF16, SQ_F32
+from ._lib import SqError, SqF8, SqMx4, SqW4, SqW8, SQ_ACT, SQ_BF16, SQ_F32
 
 
 @dataclass
@@ -575,3 +575,284 @@ def linear_fwd_mx4(x: torch.Tensor, p: MX4Payload, out_dtype=torch.float32,
                                   workspace.data_ptr(), _nbytes(workspace), _stream()),
            "sq_linear_fwd_mx4")
     return out
+
+
+# ---------------------------------------------------------------- 8-bit float mode
+@dataclass
+class F8Payload:
+    """Device tensors of one 8-bit float layer (layouts as in sq.h)."""
+    codes: torch.Tensor      # float8_e4m3fn [N, K rounded up to 128], zero from column K on
+    exps: torch.Tensor       # uint8 [ceil(N/128), ceil(K/128)]
+    k: int                   # input features
+
+    @property
+    def n(self) -> int:
+        return self.codes.shape[-2]
+
+    def abi(self) -> SqF8:
+        _require(self.codes, torch.float8_e4m3fn, "codes")
+        _require(self.exps, torch.uint8, "exps")
+        S.check_f8_payload(self.codes.shape, self.exps.shape, self.k)
+        return SqF8(self.n, self.k, self.codes.data_ptr(), self.exps.data_ptr())
+
+
+@dataclass
+class GroupedF8Payload:
+    """Device tensors of E 8-bit float layers of one shape (one per expert), stacked."""
+    codes: torch.Tensor      # float8_e4m3fn [E, N, K rounded up to 128]
+    exps: torch.Tensor       # uint8 [E, ceil(N/128), ceil(K/128)]
+    k: int
+
+    @property
+    def groups(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def n(self) -> int:
+        return self.codes.shape[-2]
+
+    def abi(self) -> SqF8:
+        _require(self.codes, torch.float8_e4m3fn, "codes")
+        _require(self.exps, torch.uint8, "exps")
+        S.check_grouped_f8_payload(self.codes.shape, self.exps.shape, self.k)
+        return SqF8(self.n, self.k, self.codes.data_ptr(), self.exps.data_ptr())
+
+
+def empty_payload_f8(n: int, k: int, device="cuda") -> F8Payload:
+    kb = -(-k // 128)
+    return F8Payload(torch.empty((n, 128 * kb), dtype=torch.float8_e4m3fn, device=device),
+                     torch.empty((-(-n // 128), kb), dtype=torch.uint8, device=device), k)
+
+
+def quantize_weight_f8(w: torch.Tensor):
+    """sq_quantize_weight_f8: W [N,K] (fp32 or bf16) -> (payload, flags tensor)."""
+    if w.dtype not in _OUT_DTYPES:
+        raise TypeError(f"w must be torch.float32 or torch.bfloat16, got {w.dtype}")
+    dev = torch.cuda.current_device()
+    _dense(w, w.dtype, "w", dev)
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D [N, K]")
+    n, k = w.shape
+    p = empty_payload_f8(n, k, w.device)
+    flags = torch.zeros(4, dtype=torch.int32, device=w.device)
+    _check(_lib.sq_quantize_weight_f8(w.data_ptr(), _OUT_DTYPES[w.dtype], p.abi(), flags.data_ptr(),
+                                      _raw_stream(dev)), "sq_quantize_weight_f8")
+    return p, flags
+
+
+def stack_payloads_f8(payloads) -> GroupedF8Payload:
+    """One GroupedF8Payload from the 8-bit float payloads of experts 0, 1, ... (copies)."""
+    payloads = list(payloads)
+    if not payloads:
+        raise ValueError("need at least one payload")
+    for p in payloads:
+        if not isinstance(p, F8Payload):
+            raise TypeError(f"experts must be F8Payload, got {type(p).__name__}")
+        if (p.n, p.k) != (payloads[0].n, payloads[0].k):
+            raise ValueError("every expert must have the same N and K")
+    return GroupedF8Payload(torch.stack([p.codes for p in payloads]),
+                            torch.stack([p.exps for p in payloads]), payloads[0].k)
+
+
+def _f8_payload(p, grouped: bool):
+    """A stack of experts and one layer share a C struct: neither is taken for the other."""
+    want = GroupedF8Payload if grouped else F8Payload
+    if not isinstance(p, want):
+        raise TypeError(f"this call takes a {want.__name__}, got {type(p).__name__}")
+
+
+def _f8_pair(gate, up, grouped: bool):
+    _f8_payload(gate, grouped)
+    _f8_payload(up, grouped)
+    if (gate.codes.shape, gate.k) != (up.codes.shape, up.k):
+        raise ValueError("gate and up must have the same shape")
+
+
+def _f8_act(act) -> int:
+    if act not in SQ_ACT:
+        raise ValueError(f"act must be one of {sorted(SQ_ACT)}, got {act!r}")
+    return SQ_ACT[act]
+
+
+def _f8_product(call, sizes, ins, cols, offsets, payloads, act, out_dtype, extra, workspace, out,
+                grouped):
+    """The common part of the 8-bit float products (checks, allocation, call).
+
+    ins: (name, tensor) of the bf16 inputs [M, cols[0]]; cols: columns of inputs and result;
+    extra: optional bf16 tensors that the call writes besides, by name, with their columns."""
+    dev = torch.cuda.current_device()
+    for name, t in ins:
+        _dense(t, torch.bfloat16, name, dev)
+        m = S.check_rows(name, t.shape, cols[0])
+        if m != ins[0][1].shape[0]:
+            raise ValueError(f"{name} must have as many rows as {ins[0][0]}")
+    abis = [p.abi() for p in payloads]
+    for p in payloads:
+        _dense(p.codes, p.codes.dtype, "the payload", dev)
+        _dense(p.exps, p.exps.dtype, "the payload", dev)
+    groups = ()
+    if grouped:
+        if offsets is None:
+            raise TypeError("grouped calls need the experts' row offsets")
+        _dense(offsets, torch.int32, "offsets", dev)
+        S.check_offsets(offsets.shape, payloads[0].groups)
+        groups = (offsets.data_ptr(), payloads[0].groups)
+    if out is None:
+        if out_dtype not in _OUT_DTYPES:
+            raise ValueError("out_dtype must be torch.float32 or torch.bfloat16")
+        out = torch.empty((m, cols[1]), dtype=out_dtype, device=ins[0][1].device)
+    else:
+        _dense(out, out.dtype, "out", dev)
+        S.check_out("out", out.shape, (m, cols[1]))
+        if out.dtype not in _OUT_DTYPES:
+            raise ValueError("out must be fp32 or bf16")
+    if workspace is None:
+        workspace = torch.empty(max(sizes(m, *groups[1:], abis[0]), 16), dtype=torch.uint8,
+                                device=out.device)
+    else:
+        _dense(workspace, workspace.dtype, "workspace", dev)
+    args = [t.data_ptr() for _, t in ins] + [m, *groups, *abis]
+    args += ([] if act is None else [act]) + [out.data_ptr(), _OUT_DTYPES[out.dtype]]
+    args += [None if t is None else t.data_ptr() for t in extra]
+    status = call(*args, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                  _raw_stream(dev))
+    if status != _lib.SQ_OK:
+        raise SqError(status, call.__name__)
+    return out
+
+
+def fwd_f8_workspace_bytes(m: int, p: F8Payload) -> int:
+    _f8_payload(p, False)
+    return _lib.sq_linear_fwd_f8_workspace_bytes(m, p.abi())
+
+
+def linear_fwd_f8(x: torch.Tensor, p: F8Payload, out_dtype=torch.float32,
+                  workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_linear_fwd_f8: bf16 x [M,K] -> y [M,N] (fp32 or bf16) for an 8-bit float payload."""
+    _f8_payload(p, False)
+    return _f8_product(_lib.sq_linear_fwd_f8, _lib.sq_linear_fwd_f8_workspace_bytes, [("x", x)],
+                       (p.k, p.n), None, [p], None, out_dtype, (), workspace, out, False)
+
+
+def dgrad_f8_workspace_bytes(m: int, p: F8Payload) -> int:
+    _f8_payload(p, False)
+    return _lib.sq_linear_dgrad_f8_workspace_bytes(m, p.abi())
+
+
+def linear_dgrad_f8(dy: torch.Tensor, p: F8Payload, out_dtype=torch.float32,
+                    workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_linear_dgrad_f8: bf16 dy [M,N] -> dx [M,K] (fp32 or bf16)."""
+    _f8_payload(p, False)
+    return _f8_product(_lib.sq_linear_dgrad_f8, _lib.sq_linear_dgrad_f8_workspace_bytes,
+                       [("dy", dy)], (p.n, p.k), None, [p], None, out_dtype, (), workspace, out,
+                       False)
+
+
+def grouped_fwd_f8_workspace_bytes(m: int, p: GroupedF8Payload) -> int:
+    _f8_payload(p, True)
+    return _lib.sq_grouped_fwd_f8_workspace_bytes(m, p.groups, p.abi())
+
+
+def grouped_fwd_f8(x: torch.Tensor, offsets: torch.Tensor, p: GroupedF8Payload,
+                   out_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None):
+    """sq_grouped_fwd_f8: rows offsets[e]..offsets[e+1]-1 of x [M,K] through expert e.
+
+    offsets as for grouped_fwd_w8a8; rows outside the experts' ranges are left as they were in
+    `out` (undefined when it is allocated here)."""
+    _f8_payload(p, True)
+    return _f8_product(_lib.sq_grouped_fwd_f8, _lib.sq_grouped_fwd_f8_workspace_bytes, [("x", x)],
+                       (p.k, p.n), offsets, [p], None, out_dtype, (), workspace, out, True)
+
+
+def grouped_dgrad_f8_workspace_bytes(m: int, p: GroupedF8Payload) -> int:
+    _f8_payload(p, True)
+    return _lib.sq_grouped_dgrad_f8_workspace_bytes(m, p.groups, p.abi())
+
+
+def grouped_dgrad_f8(dy: torch.Tensor, offsets: torch.Tensor, p: GroupedF8Payload,
+                     out_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None):
+    """sq_grouped_dgrad_f8: the input gradient of grouped_fwd_f8, rows and offsets alike."""
+    _f8_payload(p, True)
+    return _f8_product(_lib.sq_grouped_dgrad_f8, _lib.sq_grouped_dgrad_f8_workspace_bytes,
+                       [("dy", dy)], (p.n, p.k), offsets, [p], None, out_dtype, (), workspace, out,
+                       True)
+
+
+def _gated_fwd(call, sizes, x, offsets, gate, up, act, out_dtype, save, workspace, out, grouped):
+    _f8_pair(gate, up, grouped)
+    code = _f8_act(act)
+    saved = tuple(torch.empty((x.shape[0], gate.n), dtype=torch.bfloat16, device=x.device)
+                  for _ in range(2)) if save else (None, None)
+    h = _f8_product(call, sizes, [("x", x)], (gate.k, gate.n), offsets, [gate, up], code, out_dtype,
+                    saved, workspace, out, grouped)
+    return (h, *saved) if save else h
+
+
+def _gated_bwd(call, sizes, dh, g, u, offsets, gate, up, act, out_dtype, want_dgu, workspace, out,
+               grouped):
+    _f8_pair(gate, up, grouped)
+    code = _f8_act(act)
+    made = tuple(torch.empty_like(dh) for _ in range(2)) if want_dgu else (None, None)
+    dx = _f8_product(call, sizes, [("dh", dh), ("g", g), ("u", u)], (gate.n, gate.k), offsets,
+                     [gate, up], code, out_dtype, made, workspace, out, grouped)
+    return (dx, *made) if want_dgu else dx
+
+
+def gated_fwd_f8_workspace_bytes(m: int, gate: F8Payload) -> int:
+    _f8_payload(gate, False)
+    return _lib.sq_gated_fwd_f8_workspace_bytes(m, gate.abi())
+
+
+def gated_fwd_f8(x: torch.Tensor, gate: F8Payload, up: F8Payload, act: str = "silu",
+                 out_dtype=torch.float32, save: bool = False,
+                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_gated_fwd_f8: bf16 x [M,K] -> h = act(g) * u [M,N] (fp32 or bf16), g and u the products
+    of x with gate and up; act is "silu", "gelu" or "gelu_tanh".  With save: (h, g, u), g and u in
+    bf16, for gated_bwd_f8."""
+    return _gated_fwd(_lib.sq_gated_fwd_f8, _lib.sq_gated_fwd_f8_workspace_bytes, x, None, gate, up,
+                      act, out_dtype, save, workspace, out, False)
+
+
+def gated_bwd_f8_workspace_bytes(m: int, gate: F8Payload) -> int:
+    _f8_payload(gate, False)
+    return _lib.sq_gated_bwd_f8_workspace_bytes(m, gate.abi())
+
+
+def gated_bwd_f8(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, gate: F8Payload,
+                 up: F8Payload, act: str = "silu", out_dtype=torch.float32, want_dgu: bool = True,
+                 workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_gated_bwd_f8: bf16 dh, g, u [M,N] -> (dx [M,K] (fp32 or bf16), dg, du [M,N] bf16);
+    dx alone without want_dgu."""
+    return _gated_bwd(_lib.sq_gated_bwd_f8, _lib.sq_gated_bwd_f8_workspace_bytes, dh, g, u, None,
+                      gate, up, act, out_dtype, want_dgu, workspace, out, False)
+
+
+def grouped_gated_fwd_f8_workspace_bytes(m: int, gate: GroupedF8Payload) -> int:
+    _f8_payload(gate, True)
+    return _lib.sq_grouped_gated_fwd_f8_workspace_bytes(m, gate.groups, gate.abi())
+
+
+def grouped_gated_fwd_f8(x: torch.Tensor, offsets: torch.Tensor, gate: GroupedF8Payload,
+                         up: GroupedF8Payload, act: str = "silu", out_dtype=torch.float32,
+                         save: bool = False, workspace: torch.Tensor | None = None,
+                         out: torch.Tensor | None = None):
+    """sq_grouped_gated_fwd_f8: gated_fwd_f8 with rows sorted by expert, offsets as for
+    grouped_fwd_f8."""
+    return _gated_fwd(_lib.sq_grouped_gated_fwd_f8, _lib.sq_grouped_gated_fwd_f8_workspace_bytes, x,
+                      offsets, gate, up, act, out_dtype, save, workspace, out, True)
+
+
+def grouped_gated_bwd_f8_workspace_bytes(m: int, gate: GroupedF8Payload) -> int:
+    _f8_payload(gate, True)
+    return _lib.sq_grouped_gated_bwd_f8_workspace_bytes(m, gate.groups, gate.abi())
+
+
+def grouped_gated_bwd_f8(dh: torch.Tensor, g: torch.Tensor, u: torch.Tensor, offsets: torch.Tensor,
+                         gate: GroupedF8Payload, up: GroupedF8Payload, act: str = "silu",
+                         out_dtype=torch.float32, want_dgu: bool = True,
+                         workspace: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """sq_grouped_gated_bwd_f8: gated_bwd_f8 with rows sorted by expert."""
+    return _gated_bwd(_lib.sq_grouped_gated_bwd_f8, _lib.sq_grouped_gated_bwd_f8_workspace_bytes,
+                      dh, g, u, offsets, gate, up, act, out_dtype, want_dgu, workspace, out, True)

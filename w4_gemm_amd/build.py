@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "libsq.so")
 BUILD = os.path.join(HERE, "_build")
 SOURCES = ["sq_abi.hip", "sq_reconstruct.hip", "sq_quantize.hip", "sq_fwd.hip", "sq_dgrad.hip",
-           "sq_decode.hip", "sq_w8.hip", "sq_mx.hip", "sq_w8a8.hip", "sq_w8_dgrad.hip"]
+           "sq_decode.hip", "sq_w8.hip", "sq_mx.hip", "sq_w8a8.hip", "sq_w8_dgrad.hip",
+           "sq_f8_rows.hip", "sq_f8.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

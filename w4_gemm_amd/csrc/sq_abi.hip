@@ -67,6 +67,14 @@ sq_status_t check_payload_mx(const sq_mx4_t* p) {
   return SQ_OK;
 }
 
+sq_status_t check_payload_f8(const sq_f8_t* p) {
+  if (!p) return SQ_E_NULL;
+  if (p->n < 1 || p->k < 1 || p->n > SQ_F8_MAX || p->k > SQ_F8_MAX) return SQ_E_SHAPE;
+  if (!p->codes || !p->exps) return SQ_E_NULL;
+  if (!aligned16(p->codes) || !aligned16(p->exps)) return SQ_E_ALIGN;
+  return SQ_OK;
+}
+
 sq_status_t from_hip(hipError_t e) { return e == hipSuccess ? SQ_OK : SQ_E_HIP; }
 
 // Scratch of the allocation-free forward: one copy per device, part of the
@@ -103,7 +111,8 @@ const char* sq_status_str(sq_status_t s) {
     case SQ_E_SHAPE:
       return "bad shape: need K % 256 == 0, K >= 256, N >= 1, M >= 0 (W4 input gradient: N % 64 == 0; "
              "8-bit products: K <= 65536, M < 2^31, groups >= 1, their input gradient N <= 131072, "
-             "M <= 2^25 (2^23 for N > 2048))";
+             "M <= 2^25 (2^23 for N > 2048); 8-bit float mode: 1 <= N, K <= 2^20, gate and up alike, "
+             "fewer than 2^32 threads per launch)";
     case SQ_E_GROUP: return "group must be 32 or 64";
     case SQ_E_RANK: return "rank must be 0, 32 or 64 (int8 mode: 0, 16, 32 or 64; reserved 0)";
     case SQ_E_ALIGN: return "every pointer must be 16-byte aligned";
@@ -111,6 +120,7 @@ const char* sq_status_str(sq_status_t s) {
     case SQ_E_DTYPE: return "output dtype must be SQ_F32 or SQ_BF16";
     case SQ_E_ARCH: return "the current device is not gfx950 (MI355X)";
     case SQ_E_HIP: return "a HIP runtime call or kernel launch failed";
+    case SQ_E_ACT: return "activation must be SQ_ACT_SILU, SQ_ACT_GELU or SQ_ACT_GELU_TANH";
   }
   return "unknown status";
 }
@@ -448,6 +458,203 @@ sq_status_t sqi_i8_form(int64_t m, int32_t groups, const sq_w8_t* p, int32_t dgr
     memcpy(form, f, sizeof f);
   }
   return SQ_OK;
+}
+
+// ---------------------------------------------------------------- 8-bit float mode
+sq_status_t sq_quantize_weight_f8(const void* w, sq_dtype_t w_dtype, const sq_f8_t* p,
+                                  int32_t* dev_flags, void* stream) {
+  if (w_dtype != SQ_F32 && w_dtype != SQ_BF16) return SQ_E_DTYPE;
+  sq_status_t st = check_payload_f8(p);
+  if (st != SQ_OK) return st;
+  // one workgroup of 256 threads per block; a launch has fewer than 2^32 threads
+  if ((p->n + 127) / 128 * ((p->k + 127) / 128) >= int64_t{1} << 24) return SQ_E_SHAPE;
+  if (!w || !dev_flags) return SQ_E_NULL;
+  if (!aligned16(w) || !aligned16(dev_flags)) return SQ_E_ALIGN;
+  if ((st = check_device()) != SQ_OK) return st;
+  return from_hip(sq::launch_f8_weight(w, w_dtype == SQ_BF16, p->codes, p->exps, dev_flags, p->n,
+                                       p->k, static_cast<hipStream_t>(stream)));
+}
+
+static bool f8_shape_ok(int64_t m, int32_t groups) {
+  if (m < 0 || m > INT32_MAX || groups < 1) return false;
+  // offsets that are not ordered can name up to ceil(m / 16) tiles per group,
+  // which the device counts in 32 bits
+  return (m + 15) / 16 <= INT32_MAX / groups;
+}
+
+static size_t f8_workspace_bytes(int kind, int64_t m, int32_t groups, const sq_f8_t* p) {
+  if (!p || m <= 0 || p->n < 1 || p->k < 1 || p->n > SQ_F8_MAX || p->k > SQ_F8_MAX) return 0;
+  if (!f8_shape_ok(m, groups)) return 0;
+  // enough for either type of the result
+  const sq::F8Plan a = sq::plan_f8(kind, m, p->n, p->k, groups, true);
+  const sq::F8Plan b = sq::plan_f8(kind, m, p->n, p->k, groups, false);
+  if (!a.ok || !b.ok) return 0;
+  return a.total > b.total ? a.total : b.total;
+}
+
+// The common part of the products.  gate holds the one weight of a plain product;
+// c has the pointers that the kinds differ in.
+static sq_status_t f8_product(int kind, int64_t m, const int32_t* offsets, bool grouped,
+                              int32_t groups, const sq_f8_t* gate, const sq_f8_t* up, int act,
+                              sq::F8Call c, sq_dtype_t out_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  const bool gated = kind == sq::SQ_F8_GATED_FWD || kind == sq::SQ_F8_GATED_BWD;
+  if (out_dtype != SQ_F32 && out_dtype != SQ_BF16) return SQ_E_DTYPE;
+  if (gated && (act < SQ_ACT_SILU || act > SQ_ACT_GELU_TANH)) return SQ_E_ACT;
+  sq_status_t st = check_payload_f8(gate);
+  if (st == SQ_OK && gated) st = check_payload_f8(up);
+  if (st != SQ_OK) return st;
+  if (gated && (gate->n != up->n || gate->k != up->k)) return SQ_E_SHAPE;
+  if (!f8_shape_ok(m, groups)) return SQ_E_SHAPE;
+  if (m == 0) return SQ_OK;
+  const sq::F8Plan plan = sq::plan_f8(kind, m, gate->n, gate->k, groups, out_dtype == SQ_BF16);
+  if (!plan.ok) return SQ_E_SHAPE;
+  if (!c.a || !c.y || !workspace || (grouped && !offsets)) return SQ_E_NULL;
+  if (kind == sq::SQ_F8_GATED_BWD && (!c.g_in || !c.u_in)) return SQ_E_NULL;
+  if (kind == sq::SQ_F8_GATED_FWD && !c.g != !c.u) return SQ_E_NULL;
+  for (const void* ptr : {(const void*)c.a, (const void*)c.y, (const void*)workspace,
+                          (const void*)offsets, (const void*)c.g_in, (const void*)c.u_in,
+                          (const void*)c.g, (const void*)c.u, (const void*)c.dg, (const void*)c.du})
+    if (!aligned16(ptr)) return SQ_E_ALIGN;
+  if (workspace_bytes < plan.total) return SQ_E_WORKSPACE;
+  if ((st = check_device()) != SQ_OK) return st;
+  c.offsets = grouped ? offsets : nullptr;
+  c.codes[0] = gate->codes;
+  c.exps[0] = gate->exps;
+  c.codes[1] = gated ? up->codes : nullptr;
+  c.exps[1] = gated ? up->exps : nullptr;
+  c.y_bf16 = out_dtype == SQ_BF16;
+  c.act = act;
+  return from_hip(sq::launch_f8(plan, c, workspace, static_cast<hipStream_t>(stream)));
+}
+
+size_t sq_linear_fwd_f8_workspace_bytes(int64_t m, const sq_f8_t* p) {
+  return f8_workspace_bytes(sq::SQ_F8_FWD, m, 1, p);
+}
+
+sq_status_t sq_linear_fwd_f8(const uint16_t* x, int64_t m, const sq_f8_t* p, void* y,
+                             sq_dtype_t y_dtype, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  sq::F8Call c{};
+  c.a = x;
+  c.y = y;
+  return f8_product(sq::SQ_F8_FWD, m, nullptr, false, 1, p, nullptr, 0, c, y_dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t sq_linear_dgrad_f8_workspace_bytes(int64_t m, const sq_f8_t* p) {
+  return f8_workspace_bytes(sq::SQ_F8_DGRAD, m, 1, p);
+}
+
+sq_status_t sq_linear_dgrad_f8(const uint16_t* dy, int64_t m, const sq_f8_t* p, void* dx,
+                               sq_dtype_t dx_dtype, void* workspace, size_t workspace_bytes,
+                               void* stream) {
+  sq::F8Call c{};
+  c.a = dy;
+  c.y = dx;
+  return f8_product(sq::SQ_F8_DGRAD, m, nullptr, false, 1, p, nullptr, 0, c, dx_dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t sq_grouped_fwd_f8_workspace_bytes(int64_t m, int32_t groups, const sq_f8_t* p) {
+  return f8_workspace_bytes(sq::SQ_F8_FWD, m, groups, p);
+}
+
+sq_status_t sq_grouped_fwd_f8(const uint16_t* x, int64_t m, const int32_t* offsets, int32_t groups,
+                              const sq_f8_t* p, void* y, sq_dtype_t y_dtype, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  sq::F8Call c{};
+  c.a = x;
+  c.y = y;
+  return f8_product(sq::SQ_F8_FWD, m, offsets, true, groups, p, nullptr, 0, c, y_dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t sq_grouped_dgrad_f8_workspace_bytes(int64_t m, int32_t groups, const sq_f8_t* p) {
+  return f8_workspace_bytes(sq::SQ_F8_DGRAD, m, groups, p);
+}
+
+sq_status_t sq_grouped_dgrad_f8(const uint16_t* dy, int64_t m, const int32_t* offsets,
+                                int32_t groups, const sq_f8_t* p, void* dx, sq_dtype_t dx_dtype,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  sq::F8Call c{};
+  c.a = dy;
+  c.y = dx;
+  return f8_product(sq::SQ_F8_DGRAD, m, offsets, true, groups, p, nullptr, 0, c, dx_dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+size_t sq_gated_fwd_f8_workspace_bytes(int64_t m, const sq_f8_t* gate) {
+  return f8_workspace_bytes(sq::SQ_F8_GATED_FWD, m, 1, gate);
+}
+
+sq_status_t sq_gated_fwd_f8(const uint16_t* x, int64_t m, const sq_f8_t* gate, const sq_f8_t* up,
+                            sq_act_t act, void* h, sq_dtype_t h_dtype, uint16_t* g, uint16_t* u,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  sq::F8Call c{};
+  c.a = x;
+  c.y = h;
+  c.g = g;
+  c.u = u;
+  return f8_product(sq::SQ_F8_GATED_FWD, m, nullptr, false, 1, gate, up, act, c, h_dtype, workspace,
+                    workspace_bytes, stream);
+}
+
+size_t sq_gated_bwd_f8_workspace_bytes(int64_t m, const sq_f8_t* gate) {
+  return f8_workspace_bytes(sq::SQ_F8_GATED_BWD, m, 1, gate);
+}
+
+sq_status_t sq_gated_bwd_f8(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int64_t m,
+                            const sq_f8_t* gate, const sq_f8_t* up, sq_act_t act, void* dx,
+                            sq_dtype_t dx_dtype, uint16_t* dg, uint16_t* du, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  sq::F8Call c{};
+  c.a = dh;
+  c.g_in = g;
+  c.u_in = u;
+  c.y = dx;
+  c.dg = dg;
+  c.du = du;
+  return f8_product(sq::SQ_F8_GATED_BWD, m, nullptr, false, 1, gate, up, act, c, dx_dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+size_t sq_grouped_gated_fwd_f8_workspace_bytes(int64_t m, int32_t groups, const sq_f8_t* gate) {
+  return f8_workspace_bytes(sq::SQ_F8_GATED_FWD, m, groups, gate);
+}
+
+sq_status_t sq_grouped_gated_fwd_f8(const uint16_t* x, int64_t m, const int32_t* offsets,
+                                    int32_t groups, const sq_f8_t* gate, const sq_f8_t* up,
+                                    sq_act_t act, void* h, sq_dtype_t h_dtype, uint16_t* g,
+                                    uint16_t* u, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  sq::F8Call c{};
+  c.a = x;
+  c.y = h;
+  c.g = g;
+  c.u = u;
+  return f8_product(sq::SQ_F8_GATED_FWD, m, offsets, true, groups, gate, up, act, c, h_dtype,
+                    workspace, workspace_bytes, stream);
+}
+
+size_t sq_grouped_gated_bwd_f8_workspace_bytes(int64_t m, int32_t groups, const sq_f8_t* gate) {
+  return f8_workspace_bytes(sq::SQ_F8_GATED_BWD, m, groups, gate);
+}
+
+sq_status_t sq_grouped_gated_bwd_f8(const uint16_t* dh, const uint16_t* g, const uint16_t* u,
+                                    int64_t m, const int32_t* offsets, int32_t groups,
+                                    const sq_f8_t* gate, const sq_f8_t* up, sq_act_t act, void* dx,
+                                    sq_dtype_t dx_dtype, uint16_t* dg, uint16_t* du,
+                                    void* workspace, size_t workspace_bytes, void* stream) {
+  sq::F8Call c{};
+  c.a = dh;
+  c.g_in = g;
+  c.u_in = u;
+  c.y = dx;
+  c.dg = dg;
+  c.du = du;
+  return f8_product(sq::SQ_F8_GATED_BWD, m, offsets, true, groups, gate, up, act, c, dx_dtype,
+                    workspace, workspace_bytes, stream);
 }
 
 // ---------------------------------------------------------------- MXFP4 mode

@@ -1,0 +1,429 @@
+// Products of the 8-bit float mode, for one layer and for experts.  Rows a are
+// rounded to e4m3 with a power of two per 128 values along the contraction
+// (sq_f8_rows.hip), the weight's codes have one per 128 x 128:
+//
+//   forward   y = Q(x) W^T
+//   gated     h = act(g) u, g = Q(x) Wg^T, u = Q(x) Wu^T
+//   gradient  dx = Q(dy) W, and dx = Q(dg) Wg + Q(du) Wu
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 contracts one block of each operand's row
+// with both powers of two for free: they are why the mode's scales are powers of
+// two.  The instruction sums its products in groups of eight consecutive values
+// and drops what lies below 2^-13 of a group's largest product (measured: bits
+// 2^-14 down vanish, towards zero; between groups and against the accumulator
+// it keeps 24 bits).  That is 2^-17 of sum |a b| for Gaussian rows, 1.5e-5 of
+// the result's norm, up to 5e-5 where codes spread over all exponents: a
+// hundredth of a bf16 result's own rounding, and 250 times an fp32 result's.
+// So results of 16 bits take it, and fp32 results take fp16 MFMA on the codes
+// as fp16 (every e4m3 value is one; products exact, sums in fp32), with the
+// powers of two applied to each block's sum: 2.5e-7 at K = 16384, at half the
+// matrix rate.
+#include <algorithm>
+#include <type_traits>
+
+#include "sq_f8.hpp"
+#include "sq_kernels.h"
+
+namespace sq {
+namespace {
+
+enum { F8_FWD = 0, F8_GATED = 1, F8_GRAD = 2 };
+
+struct F8Args {
+  const uint8_t *a, *ax;          // rows: codes [m][128 stages], exponents [m][lax]
+  const uint8_t *b0, *b1;         // weight codes [groups][n][128 kb] (b1: up)
+  const uint8_t *x0, *x1;         // their exponents [groups][nb][kb]
+  const int32_t* offsets;
+  void* y;
+  uint16_t *g, *u;                // gated: both projections in bf16, or null
+  float* partial;
+  int groups, m, n, k, kb, nb;
+  int lax, stages;                // 128-value blocks along the contraction
+  int y_bf16, act, most_tiles, splits;
+};
+
+typedef _Float16 half16 __attribute__((ext_vector_type(16)));
+struct F16Frag {
+  half8 h[4];
+};
+// 32 codes of a lane as fp16, in order.
+__device__ __forceinline__ F16Frag f8_to_f16(const i32x8& c) {
+  F16Frag o;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const half2_t p0 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * w], 1.0f, false);
+    const half2_t p1 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * w], 1.0f, true);
+    const half2_t p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * w + 1], 1.0f, false);
+    const half2_t p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((uint32_t)c[2 * w + 1], 1.0f, true);
+    o.h[w] = (half8){p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+  }
+  return o;
+}
+__device__ __forceinline__ f32x4 f16_block(const F16Frag& w, const F16Frag& a) {
+  f32x4 p = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.h[s], a.h[s], p, 0, 0, 0);
+  return p;
+}
+// acc + p 2^(byte sum - 254)
+__device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes) {
+#pragma unroll
+  for (int v = 0; v < 4; ++v) acc[v] += __builtin_amdgcn_ldexpf(p[v], bytes - 254);
+}
+
+// ---------------------------------------------------------------- tiles
+// BM = 32 FM rows per workgroup x 256 columns of the weight tile (gated: 128
+// columns of gate and the same 128 of up), 2 x 4 waves of 16 FM x 64.  The
+// weight is the MFMA's first operand, so that a lane ends up with consecutive
+// columns of one row.  One stage = one block of 128 along the contraction, two
+// stages in LDS, global -> LDS with direct 16-byte buffer loads.
+//   rows and forward weight rows (128 bytes): chunk c of row r at slot c ^ (r & 7);
+//   gradient, weight rows of 256 bytes: slot c ^ b_swz(r), read transposed (see
+//   sq_w8_dgrad.hip).
+// Forward: LDS row 64 w + 16 j + 4 q + v of the weight holds column 64 w + 16 q
+// + 4 j + v, so lane (fr, g) holds 16 consecutive columns of row fr; gated: row
+// 64 w + 32 s + 16 j + 4 q + v holds column 32 w + 8 q + 4 j + v of gate (s = 0)
+// or up, so that a lane has eight columns of both.
+constexpr int F8_BN = 256, F8_THREADS = 512;
+constexpr int F8_BSTAGE = F8_BN * 128;
+
+__device__ __forceinline__ int grad_swz(int r) { return (r & 7) | (((r >> 4) & 1) << 3); }
+
+template <int FM, int MODE, bool F16, bool SPLIT>
+__global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
+  constexpr int BM = 32 * FM, NA = (BM + 63) / 64, A_STAGE = NA * 64 * 128;
+  constexpr int WIDTH = MODE == F8_GATED ? 128 : 256;   // columns of the result per tile
+  __shared__ __attribute__((aligned(16))) uint8_t a0[A_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t b0[F8_BSTAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t b1[F8_BSTAGE];
+  // exponents of four stages, twice: of the rows in the order [stage][wave
+  // row][fr][row tile], and of the tile's two weight blocks
+  __shared__ __attribute__((aligned(16))) uint8_t ea[2][4][256];
+  __shared__ __attribute__((aligned(16))) uint8_t eb[2][4][4];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int fr = lane & 15, g = lane >> 4;
+  const int out_cols = MODE == F8_GRAD ? p.k : p.n;
+  const int nt = (out_cols + WIDTH - 1) / WIDTH;
+  const int mt = row_tile_count(p.offsets, p.groups, p.m, BM, p.most_tiles, lane);
+  const int tiles = mt * nt;
+  const int split = __builtin_amdgcn_readfirstlane(tiles ? (int)blockIdx.x / tiles : p.splits);
+  if (split >= p.splits) return;
+  int64_t tm, tn;
+  xcd_tile((int)blockIdx.x - split * tiles, tiles, nt, tm, tn);
+  RowTile rt;
+  if (!find_row_tile(p.offsets, p.groups, p.m, BM, __builtin_amdgcn_readfirstlane((int)tm), lane, rt))
+    return;
+  const int grp = __builtin_amdgcn_readfirstlane(rt.group);
+  const int rows = __builtin_amdgcn_readfirstlane(rt.rows);
+  const int64_t m0 = __builtin_amdgcn_readfirstlane(rt.row0);
+  const int c0 = __builtin_amdgcn_readfirstlane((int)tn) * WIDTH;   // first result column
+  const int cols = min(WIDTH, out_cols - c0);
+  const int lda = 128 * p.stages, ldb = 128 * p.kb;
+  // stages st0 .. st0 + ST - 1; splits cut in fours, as the exponents' words do
+  const int quads = (p.stages + 3) >> 2;
+  const int q0 = __builtin_amdgcn_readfirstlane((int)((int64_t)split * quads / p.splits));
+  const int q1 = __builtin_amdgcn_readfirstlane((int)((int64_t)(split + 1) * quads / p.splits));
+  const int st0 = 4 * q0, ST = min(4 * q1, p.stages) - st0;
+
+  // ---- loaders
+  const int lr = 8 * wave + (lane >> 3);
+  const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (lr & 7));
+  const uint32_t off_a = (uint32_t)lr * (uint32_t)lda + chunk;
+  const uint8_t* a_base = p.a + m0 * lda;
+  const int q4 = (lr >> 2) & 3, v4 = lr & 3, j4 = lr >> 4;
+  const bool second = MODE == F8_GATED && wave >= 4;          // this wave loads up
+  const uint8_t* b_fwd = (second ? p.b1 : p.b0) + ((int64_t)grp * p.n + c0) * ldb;
+  const uint32_t off_b =
+      (uint32_t)(MODE == F8_GATED ? 8 * q4 + 4 * (j4 & 1) + v4 : 16 * q4 + 4 * j4 + v4) *
+          (uint32_t)ldb + chunk;
+  const int gr = 4 * wave + (lane >> 4);                      // gradient: weight row of 32
+  const uint32_t gchunk = 16u * (uint32_t)((lane & 15) ^ grad_swz(gr));
+  auto issue_a = [&](int st, uint8_t* ab, int i) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(a_base + (int64_t)(64 * i) * lda), (short)0, max(rows - 64 * i, 0) * lda, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(ab + (8 * i + wave) * 1024), 16, off_a,
+                                             (st0 + st) * 128, 0, 0);
+  };
+  auto issue_b = [&](int st, uint8_t* bb, int i) {
+    if constexpr (MODE == F8_GRAD) {
+      // rows past the weight's last repeat it (their row codes are zero)
+      const int s = st0 + st, seg = s >= p.nb, n0 = 128 * (s - (seg ? p.nb : 0));
+      const int left = min(p.n - n0, 128);
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)((seg ? p.b1 : p.b0) + ((int64_t)grp * p.n + n0) * ldb + c0), (short)0,
+          (left - 1) * ldb + min(256, ldb - c0), 0x00020000);
+      const uint32_t off = __umul24((uint32_t)min(32 * i + gr, left - 1), (uint32_t)ldb) + gchunk;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16, off,
+                                               0, 0, 0);
+    } else {
+      constexpr int STEP = WIDTH / 4;
+      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(b_fwd + (int64_t)(STEP * i) * ldb), (short)0, max(cols - STEP * i, 0) * ldb,
+          0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16,
+                                               off_b, (st0 + st) * 128, 0, 0);
+    }
+  };
+  auto issue = [&](int st, uint8_t* ab, uint8_t* bb) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i < NA) issue_a(st, ab, i);
+      issue_b(st, bb, i);
+    }
+  };
+  // exponents: thread r < BM has the word of row r, the next eight threads one
+  // byte of the weight each
+  uint32_t ew = 0;
+  auto load_exps = [&](int q) {
+    if (tid < BM) {
+      ew = *reinterpret_cast<const uint32_t*>(p.ax + (m0 + min(tid, rows - 1)) * p.lax + 4 * q);
+    } else if (tid < BM + 8) {
+      const int which = (tid - BM) & 1, s = min(4 * q + ((tid - BM) >> 1), p.stages - 1);
+      if constexpr (MODE == F8_FWD)
+        ew = p.x0[((int64_t)grp * p.nb + min((c0 >> 7) + which, p.nb - 1)) * p.kb + s];
+      else if constexpr (MODE == F8_GATED)
+        ew = (which ? p.x1 : p.x0)[((int64_t)grp * p.nb + (c0 >> 7)) * p.kb + s];
+      else
+        ew = (s >= p.nb ? p.x1 : p.x0)[((int64_t)grp * p.nb + (s >= p.nb ? s - p.nb : s)) * p.kb +
+                                       min((c0 >> 7) + which, p.kb - 1)];
+    }
+  };
+  auto put_exps = [&](int buf) {
+    if (tid < BM) {
+      // row 32 i + 16 w + f at [w][f][i]
+      const int at = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + (tid >> 5);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) ea[buf][s][at] = (uint8_t)(ew >> (8 * s));
+    } else if (tid < BM + 8) {
+      eb[buf][(tid - BM) >> 1][(tid - BM) & 1] = (uint8_t)ew;
+    }
+  };
+
+  issue(0, a0, b0);
+  issue(min(1, ST - 1), a1, b1);
+  load_exps(q0);
+  put_exps(0);
+
+  f32x4 acc[FM][4];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto sync = [&]() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);
+    __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  sync();
+
+  // ---- fragments: lane (fr, g) holds bytes 16 g .. and 64 + 16 g .. of its row
+  const uint32_t a_row = (uint32_t)(16 * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
+  const uint32_t slot0 = 16u * (uint32_t)(g ^ (fr & 7)), slot1 = 16u * (uint32_t)((4 + g) ^ (fr & 7));
+  const int tr_row = 16 * g + (fr >> 1), tr_swz = grad_swz(tr_row);
+  const uint32_t t_row = (uint32_t)tr_row * 256 + 8u * (uint32_t)(fr & 1);
+  auto read_a = [&](const uint8_t* ab, int i) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(ab + a_row + slot0 + i * 4096);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(ab + a_row + slot1 + i * 4096);
+    return (i32x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+  };
+  auto read_b = [&](const uint8_t* bb, int j) {
+    if constexpr (MODE == F8_GRAD) {
+      i32x2 t[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)   // rows 16 g + 8 (u & 1) + 64 (u / 2)
+        t[u] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+            (__attribute__((address_space(3))) i32x2*)(bb + t_row + (u & 1) * 2048 + (u >> 1) * 16384 +
+                                                       16 * ((4 * wn + j) ^ tr_swz)));
+      return (i32x8){t[0][0], t[0][1], t[1][0], t[1][1], t[2][0], t[2][1], t[3][0], t[3][1]};
+    } else {
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(bb + b_row + slot0 + j * 2048);
+      const i32x4 hi = *reinterpret_cast<const i32x4*>(bb + b_row + slot1 + j * 2048);
+      return (i32x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    }
+  };
+  // exponents of the lane's row tiles (byte i) and of its columns' weight block
+  // (forward, gradient: the wave's 64 columns lie in one; gated: gate, up)
+  struct Exps {
+    u32x2 rows;
+    int w[2];
+  };
+  auto read_exps = [&](Exps& e, int st) {
+    const int buf = (st >> 2) & 1, s = st & 3;
+    e.rows = *reinterpret_cast<const u32x2*>(&ea[buf][s][128 * wm + 8 * fr]);
+    if constexpr (MODE == F8_GATED) {
+      e.w[0] = eb[buf][s][0];
+      e.w[1] = eb[buf][s][1];
+    } else {
+      e.w[0] = e.w[1] = eb[buf][s][wn >> 1];
+    }
+  };
+
+  auto contract = [&](auto count) {
+    constexpr int F = decltype(count)::value;
+    auto product = [&](auto row, int j, const i32x8& w, const i32x8& a, const Exps& e) {
+      constexpr int i = decltype(row)::value;
+      const int we = e.w[j >> 1], re = (int)e.rows[i >> 2];
+      if constexpr (F16) {
+        add_scaled(acc[i][j], f16_block(f8_to_f16(w), f8_to_f16(a)), we + ((re >> (8 * (i & 3))) & 255));
+      } else {
+        acc[i][j] =
+            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc[i][j], 0, 0, 0, we, i & 3, re);
+      }
+    };
+    for (int st = 0; st < ST; ++st) {
+      uint8_t* ab = st & 1 ? a1 : a0;
+      uint8_t* bb = st & 1 ? b1 : b0;
+      if ((st & 3) == 0 && st + 4 < ST) load_exps(q0 + (st >> 2) + 1);
+      Exps e;
+      read_exps(e, st);
+      i32x8 w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = read_b(bb, j);
+#define SQ_F8_ROW(I)                                                                            \
+  if constexpr (I < F) {                                                                        \
+    const i32x8 a = read_a(ab, I);                                                              \
+    _Pragma("unroll") for (int j = 0; j < 4; ++j)                                               \
+        product(std::integral_constant<int, I>{}, j, w[j], a, e);                               \
+  }
+      SQ_F8_ROW(0) SQ_F8_ROW(1) SQ_F8_ROW(2) SQ_F8_ROW(3)
+      SQ_F8_ROW(4) SQ_F8_ROW(5) SQ_F8_ROW(6) SQ_F8_ROW(7)
+#undef SQ_F8_ROW
+      if ((st & 3) == 3 && st + 1 < ST) put_exps(((st >> 2) + 1) & 1);
+      sync();
+      issue(min(st + 2, ST - 1), ab, bb);
+    }
+  };
+  contract(std::integral_constant<int, FM>{});
+  __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
+  __builtin_amdgcn_sched_barrier(0);
+
+  // ---- acc[i][j][v]: row 32 i + 16 wm + fr
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int r = 32 * i + 16 * wm + fr;
+    if (r >= rows) continue;
+    const int64_t row = m0 + r;
+    if constexpr (MODE == F8_FWD) {
+      const int c = 64 * wn + 16 * g;
+      float o[16];
+#pragma unroll
+      for (int t = 0; t < 16; ++t) o[t] = acc[i][t >> 2][t & 3];
+      if constexpr (SPLIT)
+        store_run<16>(p.partial, ((int64_t)split * p.m + row) * p.n + c0 + c, o, cols - c, false);
+      else
+        store_run<16>(p.y, row * p.n + c0 + c, o, cols - c, p.y_bf16);
+    } else if constexpr (MODE == F8_GATED) {
+      const int c = 32 * wn + 8 * g;
+      float gv[8], uv[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        gv[t] = acc[i][t >> 2][t & 3];
+        uv[t] = acc[i][2 + (t >> 2)][t & 3];
+      }
+      if constexpr (SPLIT) {
+        const int64_t at = ((int64_t)split * p.m + row) * (2 * (int64_t)p.n) + c0 + c;
+        store_run<8>(p.partial, at, gv, cols - c, false);
+        store_run<8>(p.partial, at + p.n, uv, cols - c, false);
+      } else {
+        const int64_t at = row * p.n + c0 + c;
+        if (p.g) {
+          store_run<8>(p.g, at, gv, cols - c, true);
+          store_run<8>(p.u, at, uv, cols - c, true);
+        }
+        float h[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) h[t] = act_value(p.act, gv[t]) * uv[t];
+        store_run<8>(p.y, at, h, cols - c, p.y_bf16);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = 64 * wn + 16 * j + 4 * g;
+        const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+        if constexpr (SPLIT)
+          store_run<4>(p.partial, ((int64_t)split * p.m + row) * p.k + c0 + c, o, cols - c, false);
+        else
+          store_run<4>(p.y, row * p.k + c0 + c, o, cols - c, p.y_bf16);
+      }
+    }
+  }
+}
+
+size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+}  // namespace
+
+F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16) {
+  F8Plan p{};
+  p.kind = kind;
+  p.m = m; p.n = n; p.k = k; p.groups = groups;
+  const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
+  const bool grad = kind == SQ_F8_DGRAD || kind == SQ_F8_GATED_BWD;
+  p.stages = (int)(grad ? (kind == SQ_F8_GATED_BWD ? 2 * nb : nb) : kb);
+  p.lax = (p.stages + 3) & ~3;
+  p.f16 = !bf16;
+  p.tile_m = p.f16 || m <= 128 ? 128 : 256;
+  p.tile_n = kind == SQ_F8_GATED_FWD ? 128 : 256;
+  p.splits = 1;
+  const int64_t width = grad ? k : n;
+  const int64_t tiles = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n);
+  // a launch has fewer than 2^32 threads
+  p.ok = tiles * p.splits < ((int64_t)1 << 32) / F8_THREADS &&
+         f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < ((int64_t)1 << 32) / 256;
+  size_t off = 0;
+  p.off_codes = off; off = align256(off + (size_t)m * p.stages * 128);
+  p.off_exps = off;  off = align256(off + (size_t)m * p.lax);
+  p.off_part = off;  off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * width * 4 : 0));
+  p.total = off;
+  return p;
+}
+
+hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStream_t stream) {
+  char* base = static_cast<char*>(workspace);
+  uint8_t* codes = reinterpret_cast<uint8_t*>(base + p.off_codes);
+  uint8_t* exps = reinterpret_cast<uint8_t*>(base + p.off_exps);
+  const bool grad = p.kind == SQ_F8_DGRAD || p.kind == SQ_F8_GATED_BWD;
+  hipError_t err =
+      p.kind == SQ_F8_GATED_BWD
+          ? launch_f8_gated_rows(c.a, c.g_in, c.u_in, c.act, c.offsets, p.groups, codes, exps, c.dg,
+                                 c.du, p.m, p.n, p.lax, stream)
+          : launch_f8_rows(c.a, c.offsets, p.groups, codes, exps, p.m, grad ? p.n : p.k, p.lax, stream);
+  if (err != hipSuccess) return err;
+  F8Args a{};
+  a.a = codes; a.ax = exps;
+  a.b0 = c.codes[0]; a.b1 = c.codes[1];
+  a.x0 = c.exps[0]; a.x1 = c.exps[1];
+  a.offsets = c.offsets;
+  a.y = c.y; a.g = c.g; a.u = c.u;
+  a.partial = reinterpret_cast<float*>(base + p.off_part);
+  a.groups = p.groups; a.m = (int)p.m; a.n = (int)p.n; a.k = (int)p.k;
+  a.kb = (int)((p.k + 127) / 128); a.nb = (int)((p.n + 127) / 128);
+  a.lax = p.lax; a.stages = p.stages;
+  a.y_bf16 = c.y_bf16; a.act = c.act;
+  a.most_tiles = (int)i8_tile_bound(p.m, p.groups, p.tile_m);
+  a.splits = p.splits;
+  const int64_t width = grad ? p.k : p.n;
+  const int64_t tiles = a.most_tiles * ((width + p.tile_n - 1) / p.tile_n);
+  const dim3 grid((unsigned)(tiles * p.splits)), block(F8_THREADS);
+#define SQ_F8_GEMM(FM, MODE, F16) \
+  hipLaunchKernelGGL((k_f8_gemm<FM, MODE, F16, false>), grid, block, 0, stream, a)
+#define SQ_F8_MODE(MODE)                          \
+  do {                                            \
+    if (p.f16) SQ_F8_GEMM(4, MODE, true);         \
+    else if (p.tile_m == 128) SQ_F8_GEMM(4, MODE, false); \
+    else SQ_F8_GEMM(8, MODE, false);              \
+  } while (0)
+  if (grad) SQ_F8_MODE(F8_GRAD);
+  else if (p.kind == SQ_F8_GATED_FWD) SQ_F8_MODE(F8_GATED);
+  else SQ_F8_MODE(F8_FWD);
+#undef SQ_F8_MODE
+#undef SQ_F8_GEMM
+  return hipGetLastError();
+}
+
+}  // namespace sq

@@ -145,4 +145,38 @@ hipError_t launch_w8_dgrad(const W8DgradPlan& plan, const uint16_t* dy, const in
                            const uint16_t* down, void* dx, int dx_bf16, void* workspace,
                            hipStream_t stream);
 
+// 8-bit float mode (e4m3 codes, E8M0 exponents of blocks of 128).  Quantizers:
+hipError_t launch_f8_weight(const void* w, int w_bf16, uint8_t* codes, uint8_t* exps,
+                            int32_t* flags, int64_t n, int64_t k, hipStream_t stream);
+int64_t f8_rows_blocks(int64_t m, int64_t cols, bool gated);   // workgroups of the two below
+hipError_t launch_f8_rows(const uint16_t* x, const int32_t* offsets, int groups, uint8_t* codes,
+                          uint8_t* exps, int64_t m, int64_t k, int lax, hipStream_t stream);
+hipError_t launch_f8_gated_rows(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
+                                const int32_t* offsets, int groups, uint8_t* codes, uint8_t* exps,
+                                uint16_t* dg, uint16_t* du, int64_t m, int64_t n, int lax,
+                                hipStream_t stream);
+
+// Products: n and k are the weight's, offsets == null is one layer.
+enum { SQ_F8_FWD = 0, SQ_F8_DGRAD = 1, SQ_F8_GATED_FWD = 2, SQ_F8_GATED_BWD = 3 };
+struct F8Plan {
+  int kind, groups;
+  int64_t m, n, k;
+  int stages, lax;       // 128-value blocks along the contraction; bytes of a row's exponents
+  bool f16;              // fp32 results: fp16 MFMA
+  int tile_m, tile_n;
+  int splits;            // of the contraction
+  bool ok;               // false: a launch would pass 2^32 threads
+  size_t off_codes, off_exps, off_part, total;
+};
+F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16);
+struct F8Call {
+  const uint16_t *a, *g_in, *u_in;          // x or dy or dh; gated backward: saved g and u
+  const int32_t* offsets;
+  const uint8_t *codes[2], *exps[2];        // of the weight; gated: gate, up
+  void* y;
+  uint16_t *g, *u, *dg, *du;                // where wanted
+  int y_bf16, act;
+};
+hipError_t launch_f8(const F8Plan& plan, const F8Call& call, void* workspace, hipStream_t stream);
+
 }  // namespace sq

@@ -103,6 +103,32 @@ def check_mx4_payload(codes, exps, up, down) -> tuple:
     return n, k, r
 
 
+def check_f8_payload(codes, exps, k: int) -> tuple:
+    """8-bit float payload: codes e4m3 [N, K to the next 128], exps u8 [ceil(N/128), ceil(K/128)].
+    Returns (n, k)."""
+    codes = _shape(codes)
+    if len(codes) != 2:
+        raise ValueError("codes must be 2-D [N, K rounded up to 128]")
+    n, kb = codes[0], -(-k // 128)
+    if n < 1 or k < 1 or n > 1 << 20 or k > 1 << 20:
+        raise ValueError(f"need N and K from 1 to 2^20, got N={n} K={k}")
+    _need("codes", codes, (n, 128 * kb))
+    _need("exps", exps, (-(-n // 128), kb))
+    return n, k
+
+
+def check_grouped_f8_payload(codes, exps, k: int) -> tuple:
+    """Stacked 8-bit float payloads of E experts: codes [E, N, K to the next 128],
+    exps [E, ceil(N/128), ceil(K/128)].  Returns (groups, n, k)."""
+    codes, exps = _shape(codes), _shape(exps)
+    if len(codes) != 3 or codes[0] < 1:
+        raise ValueError("codes must be 3-D [E, N, K rounded up to 128] with E >= 1")
+    if len(exps) != 3 or exps[0] != codes[0]:
+        raise ValueError(f"exps must be 3-D [E, ., .] with E = {codes[0]}")
+    n, k = check_f8_payload(codes[1:], exps[1:], k)
+    return codes[0], n, k
+
+
 def check_rows(name: str, a, cols: int) -> int:
     """a must be 2-D [M, cols]; returns M."""
     a = _shape(a)

@@ -86,6 +86,7 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes
 // or up, so that a lane has eight columns of both.
 constexpr int F8_BN = 256, F8_THREADS = 512;
 constexpr int F8_BSTAGE = F8_BN * 128;
+constexpr int F8_MAX_STAGES = 4096;   // of one workgroup: the planner splits longer contractions
 
 __device__ __forceinline__ int grad_swz(int r) { return (r & 7) | (((r >> 4) & 1) << 3); }
 
@@ -97,10 +98,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b0[F8_BSTAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b1[F8_BSTAGE];
-  // exponents of four stages, twice: of the rows in the order [stage][wave
-  // row][fr][row tile], and of the tile's two weight blocks
+  // exponents: the rows' of four stages, twice, in the order [stage][wave
+  // row][fr][row tile]; all of the tile's two weight blocks'
   __shared__ __attribute__((aligned(16))) uint8_t ea[2][4][256];
-  __shared__ __attribute__((aligned(16))) uint8_t eb[2][4][4];
+  __shared__ __attribute__((aligned(16))) uint8_t eb[F8_MAX_STAGES][2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -174,37 +175,35 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
       issue_b(st, bb, i);
     }
   };
-  // exponents: thread r < BM has the word of row r, the next eight threads one
-  // byte of the weight each
-  uint32_t ew = 0;
-  auto load_exps = [&](int q) {
-    if (tid < BM) {
-      ew = *reinterpret_cast<const uint32_t*>(p.ax + (m0 + min(tid, rows - 1)) * p.lax + 4 * q);
-    } else if (tid < BM + 8) {
-      const int which = (tid - BM) & 1, s = min(4 * q + ((tid - BM) >> 1), p.stages - 1);
-      if constexpr (MODE == F8_FWD)
-        ew = p.x0[((int64_t)grp * p.nb + min((c0 >> 7) + which, p.nb - 1)) * p.kb + s];
-      else if constexpr (MODE == F8_GATED)
-        ew = (which ? p.x1 : p.x0)[((int64_t)grp * p.nb + (c0 >> 7)) * p.kb + s];
-      else
-        ew = (s >= p.nb ? p.x1 : p.x0)[((int64_t)grp * p.nb + (s >= p.nb ? s - p.nb : s)) * p.kb +
-                                       min((c0 >> 7) + which, p.kb - 1)];
-    }
-  };
+  // row exponents: every thread has the word of one row (some rows twice)
+  constexpr int EROWS = BM <= 64 ? 64 : BM <= 128 ? 128 : 256;
+  const int erow = tid & (EROWS - 1), e_at = ((erow >> 4) & 1) * 128 + (erow & 15) * 8 + (erow >> 5);
+  const uint8_t* e_src = p.ax + (m0 + min(erow, rows - 1)) * p.lax;
+  uint32_t ew;
+  auto load_exps = [&](int q) { ew = *reinterpret_cast<const uint32_t*>(e_src + 4 * min(q, quads - 1)); };
   auto put_exps = [&](int buf) {
-    if (tid < BM) {
-      // row 32 i + 16 w + f at [w][f][i]
-      const int at = ((tid >> 4) & 1) * 128 + (tid & 15) * 8 + (tid >> 5);
 #pragma unroll
-      for (int s = 0; s < 4; ++s) ea[buf][s][at] = (uint8_t)(ew >> (8 * s));
-    } else if (tid < BM + 8) {
-      eb[buf][(tid - BM) >> 1][(tid - BM) & 1] = (uint8_t)ew;
+    for (int s = 0; s < 4; ++s) ea[buf][s][e_at] = (uint8_t)(ew >> (8 * s));
+  };
+  auto weight_exps = [&]() {
+    for (int t = tid; t < 2 * ST; t += F8_THREADS) {
+      const int which = t & 1, s = st0 + (t >> 1);
+      uint8_t v;
+      if constexpr (MODE == F8_FWD)
+        v = p.x0[((int64_t)grp * p.nb + min((c0 >> 7) + which, p.nb - 1)) * p.kb + s];
+      else if constexpr (MODE == F8_GATED)
+        v = (which ? p.x1 : p.x0)[((int64_t)grp * p.nb + (c0 >> 7)) * p.kb + s];
+      else
+        v = (s >= p.nb ? p.x1 : p.x0)[((int64_t)grp * p.nb + (s >= p.nb ? s - p.nb : s)) * p.kb +
+                                      min((c0 >> 7) + which, p.kb - 1)];
+      eb[t >> 1][which] = v;
     }
   };
 
   issue(0, a0, b0);
   issue(min(1, ST - 1), a1, b1);
   load_exps(q0);
+  weight_exps();
   put_exps(0);
 
   f32x4 acc[FM][4];
@@ -253,52 +252,110 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
     int w[2];
   };
   auto read_exps = [&](Exps& e, int st) {
-    const int buf = (st >> 2) & 1, s = st & 3;
-    e.rows = *reinterpret_cast<const u32x2*>(&ea[buf][s][128 * wm + 8 * fr]);
+    e.rows = *reinterpret_cast<const u32x2*>(&ea[(st >> 2) & 1][st & 3][128 * wm + 8 * fr]);
     if constexpr (MODE == F8_GATED) {
-      e.w[0] = eb[buf][s][0];
-      e.w[1] = eb[buf][s][1];
+      e.w[0] = eb[st][0];
+      e.w[1] = eb[st][1];
     } else {
-      e.w[0] = e.w[1] = eb[buf][s][wn >> 1];
+      e.w[0] = e.w[1] = eb[st][wn >> 1];
     }
   };
 
+  // n LDS reads among m MFMAs of one region
+  auto interleave = [&](int reads, int mfmas) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < reads) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  };
   auto contract = [&](auto count) {
     constexpr int F = decltype(count)::value;
-    auto product = [&](auto row, int j, const i32x8& w, const i32x8& a, const Exps& e) {
-      constexpr int i = decltype(row)::value;
+    constexpr int NP = (F + 1) / 2;   // pairs of row tiles
+    auto product = [&](int i, int j, const i32x8& w, const i32x8& a, const Exps& e) {
       const int we = e.w[j >> 1], re = (int)e.rows[i >> 2];
       if constexpr (F16) {
         add_scaled(acc[i][j], f16_block(f8_to_f16(w), f8_to_f16(a)), we + ((re >> (8 * (i & 3))) & 255));
       } else {
-        acc[i][j] =
-            __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc[i][j], 0, 0, 0, we, i & 3, re);
+#define SQ_F8_MFMA(B) __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc[i][j], 0, 0, 0, we, B, re)
+        switch (i & 3) {
+          case 0: acc[i][j] = SQ_F8_MFMA(0); break;
+          case 1: acc[i][j] = SQ_F8_MFMA(1); break;
+          case 2: acc[i][j] = SQ_F8_MFMA(2); break;
+          default: acc[i][j] = SQ_F8_MFMA(3); break;
+        }
+#undef SQ_F8_MFMA
       }
     };
-    for (int st = 0; st < ST; ++st) {
-      uint8_t* ab = st & 1 ? a1 : a0;
-      uint8_t* bb = st & 1 ? b1 : b0;
-      if ((st & 3) == 0 && st + 4 < ST) load_exps(q0 + (st >> 2) + 1);
-      Exps e;
-      read_exps(e, st);
-      i32x8 w[4];
+    // One stage, a pair of row tiles at a time: the pair in registers is
+    // contracted while the next one is read.  When the last pair is in
+    // registers every wave has read all of the stage, so its buffers take stage
+    // st + 2, and stage st + 1 has landed: its first pair and its column tiles
+    // are read under the last pair's MFMAs, as the registers fall free.  Loads
+    // past the last stage fetch it again, into buffers that are not read any
+    // more.
+    i32x8 a[2][2], w[4];
+    Exps e, en;
+    read_exps(e, 0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = read_b(bb, j);
-#define SQ_F8_ROW(I)                                                                            \
-  if constexpr (I < F) {                                                                        \
-    const i32x8 a = read_a(ab, I);                                                              \
-    _Pragma("unroll") for (int j = 0; j < 4; ++j)                                               \
-        product(std::integral_constant<int, I>{}, j, w[j], a, e);                               \
-  }
-      SQ_F8_ROW(0) SQ_F8_ROW(1) SQ_F8_ROW(2) SQ_F8_ROW(3)
-      SQ_F8_ROW(4) SQ_F8_ROW(5) SQ_F8_ROW(6) SQ_F8_ROW(7)
-#undef SQ_F8_ROW
-      if ((st & 3) == 3 && st + 1 < ST) put_exps(((st >> 2) + 1) & 1);
+    for (int i = 0; i < 2; ++i) a[0][i] = read_a(a0, i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = read_b(b0, j);
+    // s: the stage's number modulo four.  No branches: the compiler would move
+    // MFMAs across them.
+    auto stage = [&](int st, int s) {
+      uint8_t *ab = s & 1 ? a1 : a0, *bb = s & 1 ? b1 : b0;
+      const uint8_t *an = s & 1 ? a0 : a1, *bn = s & 1 ? b0 : b1;
+      const int parity = s * NP;   // where the stage's first pair sits
+      if (s == 0) load_exps(q0 + (st >> 2) + 1);
+#pragma unroll
+      for (int q = 0; q + 1 < NP; ++q) {
+        const int cur = (q + parity) & 1;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (2 * q + 2 + i < F) a[cur ^ 1][i] = read_a(ab, 2 * q + 2 + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) product(2 * q + i, j, w[j], a[cur][i], e);
+        interleave(4, 8);
+      }
+      if (s == 3) put_exps(((st >> 2) + 1) & 1);
       sync();
-      issue(min(st + 2, ST - 1), ab, bb);
+      const int ahead = min(st + 2, ST - 1), last = (NP - 1 + parity) & 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < NA) issue_a(ahead, ab, j);
+        issue_b(ahead, bb, j);
+        if (j < 2 && j < F) a[last ^ 1][j] = read_a(an, j);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (2 * NP - 2 + i < F) product(2 * NP - 2 + i, j, w[j], a[last][i], e);
+        if (j == 2) read_exps(en, min(st + 1, ST - 1));
+        __builtin_amdgcn_sched_barrier(0);
+        w[j] = read_b(bn, j);
+      }
+      e = en;
+    };
+    int st = 0;
+    for (; st + 4 <= ST; st += 4) {
+      stage(st, 0);
+      stage(st + 1, 1);
+      stage(st + 2, 2);
+      stage(st + 3, 3);
     }
+    if (st < ST) stage(st, 0);
+    if (st + 1 < ST) stage(st + 1, 1);
+    if (st + 2 < ST) stage(st + 2, 2);
   };
-  contract(std::integral_constant<int, FM>{});
+  // a group's last tile is often half empty: it contracts half the row tiles
+  constexpr int HALF = (FM + 1) / 2;
+  if (FM >= 4 && rows <= 32 * HALF)
+    contract(std::integral_constant<int, HALF>{});
+  else
+    contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
   __builtin_amdgcn_sched_barrier(0);
 
@@ -354,9 +411,68 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   }
 }
 
+// Sum of the splits' results in order, and what the tiles' epilogue does.  A
+// workgroup takes 16 rows of one group x 64 columns, a thread four columns.
+template <bool GATED>
+__global__ void __launch_bounds__(256) k_f8_join(const float* __restrict__ partial,
+                                                 const int32_t* __restrict__ offsets, int groups,
+                                                 void* __restrict__ y, uint16_t* __restrict__ g_out,
+                                                 uint16_t* __restrict__ u_out, int m, int width,
+                                                 int splits, int y_bf16, int act) {
+  const int tid = threadIdx.x, nt = (width + 63) >> 6, tile = (int)blockIdx.x / nt;
+  RowTile rt;
+  if (!find_row_tile(offsets, groups, m, 16, tile, tid & 63, rt)) return;
+  const int lrow = tid >> 4, c = ((int)blockIdx.x - tile * nt) * 64 + 4 * (tid & 15);
+  const int left = width - c;
+  if (lrow >= rt.rows || left <= 0) return;
+  const int64_t row = rt.row0 + lrow, pitch = (int64_t)width * (GATED ? 2 : 1);
+  auto sum = [&](int64_t col, float (&o)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = 0.0f;
+    for (int s0 = 0; s0 < splits; s0 += 8) {
+      float v[8][4];
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const float* src = partial + ((int64_t)min(s0 + s, splits - 1) * m + row) * pitch + col;
+        if (left >= 4) {
+          __builtin_memcpy(v[s], src, 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[s][i] = i < left ? src[i] : 0.0f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += s0 + s < splits ? v[s][i] : 0.0f;
+    }
+  };
+  float o[4];
+  sum(c, o);
+  if constexpr (GATED) {
+    float u[4];
+    sum(width + c, u);
+    if (g_out) {
+      store_run<4>(g_out, row * width + c, o, left, true);
+      store_run<4>(u_out, row * width + c, u, left, true);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = act_value(act, o[i]) * u[i];
+  }
+  store_run<4>(y, row * width + c, o, left, y_bf16);
+}
+
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
+
+// Tile height and splits of the contraction by modelled time.
+struct F8Tile {
+  int rows;
+  double fixed, stage;   // us per round, us per stage and round
+};
+constexpr F8Tile kF8Tiles[] = {{64, 6.0, 0.45}, {128, 7.0, 0.65}, {224, 9.0, 1.05}, {256, 9.0, 1.15}};
+constexpr F8Tile kF16Tiles[] = {{64, 6.0, 0.8}, {128, 7.0, 1.4}};
 
 F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16) {
   F8Plan p{};
@@ -364,21 +480,39 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   p.m = m; p.n = n; p.k = k; p.groups = groups;
   const int64_t kb = (k + 127) / 128, nb = (n + 127) / 128;
   const bool grad = kind == SQ_F8_DGRAD || kind == SQ_F8_GATED_BWD;
+  const bool gated = kind == SQ_F8_GATED_FWD;
   p.stages = (int)(grad ? (kind == SQ_F8_GATED_BWD ? 2 * nb : nb) : kb);
   p.lax = (p.stages + 3) & ~3;
   p.f16 = !bf16;
-  p.tile_m = p.f16 || m <= 128 ? 128 : 256;
-  p.tile_n = kind == SQ_F8_GATED_FWD ? 128 : 256;
-  p.splits = 1;
-  const int64_t width = grad ? k : n;
-  const int64_t tiles = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n);
+  p.tile_n = gated ? 128 : 256;
+  const int64_t width = grad ? k : n, nt = (width + p.tile_n - 1) / p.tile_n;
+  const int quads = (p.stages + 3) / 4, least = (p.stages + F8_MAX_STAGES - 1) / F8_MAX_STAGES;
+  double best = 1e30;
+  auto consider = [&](const F8Tile& t) {
+    const double tiles = i8_expected_tiles(m, groups, t.rows) * (double)nt / 256.0;
+    for (int s = least; s <= std::min(quads, std::max(16, least)); ++s) {
+      double us = std::ceil(tiles * s) * (t.fixed + t.stage * (double)p.stages / s);
+      if (s > 1) us += 5.0 + (double)m * (double)width * (gated ? 2 : 1) * s * 8e-6 / 4.0;
+      if (us < best) {
+        best = us;
+        p.tile_m = t.rows;
+        p.splits = s;
+      }
+    }
+  };
+  if (p.f16)
+    for (const F8Tile& t : kF16Tiles) consider(t);
+  else
+    for (const F8Tile& t : kF8Tiles) consider(t);
   // a launch has fewer than 2^32 threads
-  p.ok = tiles * p.splits < ((int64_t)1 << 32) / F8_THREADS &&
+  p.ok = i8_tile_bound(m, groups, p.tile_m) * nt * p.splits < ((int64_t)1 << 32) / F8_THREADS &&
+         i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < ((int64_t)1 << 32) / 256 &&
          f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < ((int64_t)1 << 32) / 256;
   size_t off = 0;
   p.off_codes = off; off = align256(off + (size_t)m * p.stages * 128);
   p.off_exps = off;  off = align256(off + (size_t)m * p.lax);
-  p.off_part = off;  off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * width * 4 : 0));
+  p.off_part = off;
+  off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * width * (gated ? 8 : 4) : 0));
   p.total = off;
   return p;
 }
@@ -410,19 +544,38 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
   const int64_t width = grad ? p.k : p.n;
   const int64_t tiles = a.most_tiles * ((width + p.tile_n - 1) / p.tile_n);
   const dim3 grid((unsigned)(tiles * p.splits)), block(F8_THREADS);
-#define SQ_F8_GEMM(FM, MODE, F16) \
-  hipLaunchKernelGGL((k_f8_gemm<FM, MODE, F16, false>), grid, block, 0, stream, a)
-#define SQ_F8_MODE(MODE)                          \
-  do {                                            \
-    if (p.f16) SQ_F8_GEMM(4, MODE, true);         \
-    else if (p.tile_m == 128) SQ_F8_GEMM(4, MODE, false); \
-    else SQ_F8_GEMM(8, MODE, false);              \
+#define SQ_F8_GEMM(FM, MODE, F16, SPLIT) \
+  hipLaunchKernelGGL((k_f8_gemm<FM, MODE, F16, SPLIT>), grid, block, 0, stream, a)
+#define SQ_F8_FORM(MODE, SPLIT)                                          \
+  do {                                                                   \
+    if (p.f16 && p.tile_m == 64) SQ_F8_GEMM(2, MODE, true, SPLIT);       \
+    else if (p.f16) SQ_F8_GEMM(4, MODE, true, SPLIT);                    \
+    else if (p.tile_m == 64) SQ_F8_GEMM(2, MODE, false, SPLIT);          \
+    else if (p.tile_m == 128) SQ_F8_GEMM(4, MODE, false, SPLIT);         \
+    else if (p.tile_m == 224) SQ_F8_GEMM(7, MODE, false, SPLIT);         \
+    else SQ_F8_GEMM(8, MODE, false, SPLIT);                              \
+  } while (0)
+#define SQ_F8_MODE(MODE)                        \
+  do {                                          \
+    if (p.splits > 1) SQ_F8_FORM(MODE, true);   \
+    else SQ_F8_FORM(MODE, false);               \
   } while (0)
   if (grad) SQ_F8_MODE(F8_GRAD);
   else if (p.kind == SQ_F8_GATED_FWD) SQ_F8_MODE(F8_GATED);
   else SQ_F8_MODE(F8_FWD);
 #undef SQ_F8_MODE
+#undef SQ_F8_FORM
 #undef SQ_F8_GEMM
+  if (p.splits > 1) {
+    if ((err = hipGetLastError()) != hipSuccess) return err;
+    const dim3 jgrid((unsigned)(i8_tile_bound(p.m, p.groups, 16) * ((width + 63) / 64)));
+    if (p.kind == SQ_F8_GATED_FWD)
+      hipLaunchKernelGGL(k_f8_join<true>, jgrid, dim3(256), 0, stream, a.partial, c.offsets, p.groups,
+                         c.y, c.g, c.u, (int)p.m, (int)width, p.splits, c.y_bf16, c.act);
+    else
+      hipLaunchKernelGGL(k_f8_join<false>, jgrid, dim3(256), 0, stream, a.partial, c.offsets,
+                         p.groups, c.y, nullptr, nullptr, (int)p.m, (int)width, p.splits, c.y_bf16, 0);
+  }
   return hipGetLastError();
 }
 

@@ -38,7 +38,7 @@ struct F8Args {
   uint16_t *g, *u;                // gated: both projections in bf16, or null
   float* partial;
   int groups, m, n, k, kb, nb;
-  int lax, stages;                // 128-value blocks along the contraction
+  int lax, pitch, stages;         // bytes of a row's exponents; blocks of 128 of a row's codes; of the contraction
   int y_bf16, act, most_tiles, splits;
 };
 
@@ -72,30 +72,58 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes
 }
 
 // ---------------------------------------------------------------- tiles
+// Large tiles (224 and 256 rows) run on four waves, one per SIMD, with 128 columns
+// each: per MFMA they read two thirds of what eight waves of 64 columns read from
+// LDS, whose reads and the loads' writes otherwise take as long as the matrix unit
+// (4480 x 6144 x 16384: 396 -> 378 us).  Rows of codes are an odd number of
+// 128-byte blocks apart in the workspace (gated, above: 941 -> 906 us).
 // BM = 32 FM rows per workgroup x 256 columns of the weight tile (gated: 128
-// columns of gate and the same 128 of up), 2 x 4 waves of 16 FM x 64.  The
-// weight is the MFMA's first operand, so that a lane ends up with consecutive
-// columns of one row.  One stage = one block of 128 along the contraction, two
-// stages in LDS, global -> LDS with direct 16-byte buffer loads.
+// columns of gate and the same 128 of up), two wave rows of 16 FM x WN wave
+// columns of 16 FN.  The weight is the MFMA's first operand, so that a lane ends
+// up with consecutive columns of one row.  One stage = one block of 128 along
+// the contraction, two stages in LDS, global -> LDS with direct 16-byte buffer
+// loads.
 //   rows and forward weight rows (128 bytes): chunk c of row r at slot c ^ (r & 7);
-//   gradient, weight rows of 256 bytes: slot c ^ b_swz(r), read transposed (see
-//   sq_w8_dgrad.hip).
-// Forward: LDS row 64 w + 16 j + 4 q + v of the weight holds column 64 w + 16 q
-// + 4 j + v, so lane (fr, g) holds 16 consecutive columns of row fr; gated: row
-// 64 w + 32 s + 16 j + 4 q + v holds column 32 w + 8 q + 4 j + v of gate (s = 0)
-// or up, so that a lane has eight columns of both.
-constexpr int F8_BN = 256, F8_THREADS = 512;
+//   gradient, weight rows of 256 bytes: slot c ^ grad_swz(r), read transposed
+//   (see sq_w8_dgrad.hip).
+// Forward: row 16 j + 4 q + v of a wave column's LDS rows holds its column 4 FN q
+// + 4 j + v, so lane (fr, g) holds 4 FN consecutive columns of row fr; gated: the
+// first half of them gate's, the second the same of up.
+constexpr int F8_BN = 256;
 constexpr int F8_BSTAGE = F8_BN * 128;
+constexpr int F8_MAX_THREADS = 512;
 constexpr int F8_MAX_STAGES = 4096;   // of one workgroup: the planner splits longer contractions
 
 __device__ __forceinline__ int grad_swz(int r) { return (r & 7) | (((r >> 4) & 1) << 3); }
 
-template <int FM, int MODE, bool F16, bool SPLIT>
-__global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
-  constexpr int BM = 32 * FM, NA = (BM + 63) / 64, A_STAGE = NA * 64 * 128;
+// acc += w a on AGPRs that stay in place.  (Through the builtin the compiler
+// permutes 224 or more accumulators: 1.7 moves per MFMA.)  The compiler knows of
+// no hazard around it: the s_nop covers an operand that a vector instruction has
+// just written (it costs nothing measurable: an MFMA takes 32 cycles); results
+// are read behind the contraction only, after 32 wait states.
+template <int B>
+__device__ __forceinline__ void pinned_mfma(f32x4& acc, const i32x8& w, const i32x8& a, int we,
+                                            int re) {
+  asm("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel:[0,%5,0] "
+      "op_sel_hi:[0,%6,0]"
+      : "+a"(acc)
+      : "v"(w), "v"(a), "v"(we), "v"(re), "n"(B & 1), "n"(B >> 1));
+}
+
+template <int FM, int WN, int MODE, bool F16, bool SPLIT>
+__global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
+  constexpr int WAVES = 2 * WN, THREADS = 64 * WAVES, FN = 16 / WN, BM = 32 * FM;
+  // one load instruction of every wave covers LOAD rows of 128 bytes
+  constexpr int LOAD = 8 * WAVES, NA = (BM + LOAD - 1) / LOAD, NB = F8_BN / LOAD;
+  // row tiles 0 to 3 and the others apart: the compiler waits for every load into
+  // an LDS array before it reads from that array
+  constexpr int LOW = BM < 128 ? BM : 128, HIGH = BM > 128 ? NA * LOAD - 128 : 16;
+  constexpr bool PINNED = WN == 2;
   constexpr int WIDTH = MODE == F8_GATED ? 128 : 256;   // columns of the result per tile
-  __shared__ __attribute__((aligned(16))) uint8_t a0[A_STAGE];
-  __shared__ __attribute__((aligned(16))) uint8_t a1[A_STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t a0[LOW * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[LOW * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t a0_high[HIGH * 128];
+  __shared__ __attribute__((aligned(16))) uint8_t a1_high[HIGH * 128];
   __shared__ __attribute__((aligned(16))) uint8_t b0[F8_BSTAGE];
   __shared__ __attribute__((aligned(16))) uint8_t b1[F8_BSTAGE];
   // exponents: the rows' of four stages, twice, in the order [stage][wave
@@ -104,7 +132,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   __shared__ __attribute__((aligned(16))) uint8_t eb[F8_MAX_STAGES][2];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / WN, wn = wave % WN;
   const int fr = lane & 15, g = lane >> 4;
   const int out_cols = MODE == F8_GRAD ? p.k : p.n;
   const int nt = (out_cols + WIDTH - 1) / WIDTH;
@@ -122,7 +150,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   const int64_t m0 = __builtin_amdgcn_readfirstlane(rt.row0);
   const int c0 = __builtin_amdgcn_readfirstlane((int)tn) * WIDTH;   // first result column
   const int cols = min(WIDTH, out_cols - c0);
-  const int lda = 128 * p.stages, ldb = 128 * p.kb;
+  const int lda = 128 * p.pitch, ldb = 128 * p.kb;
   // stages st0 .. st0 + ST - 1; splits cut in fours, as the exponents' words do
   const int quads = (p.stages + 3) >> 2;
   const int q0 = __builtin_amdgcn_readfirstlane((int)((int64_t)split * quads / p.splits));
@@ -134,46 +162,71 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   const uint32_t chunk = 16u * (uint32_t)((lane & 7) ^ (lr & 7));
   const uint32_t off_a = (uint32_t)lr * (uint32_t)lda + chunk;
   const uint8_t* a_base = p.a + m0 * lda;
-  const int q4 = (lr >> 2) & 3, v4 = lr & 3, j4 = lr >> 4;
-  const bool second = MODE == F8_GATED && wave >= 4;          // this wave loads up
-  const uint8_t* b_fwd = (second ? p.b1 : p.b0) + ((int64_t)grp * p.n + c0) * ldb;
-  const uint32_t off_b =
-      (uint32_t)(MODE == F8_GATED ? 8 * q4 + 4 * (j4 & 1) + v4 : 16 * q4 + 4 * j4 + v4) *
-          (uint32_t)ldb + chunk;
-  const int gr = 4 * wave + (lane >> 4);                      // gradient: weight row of 32
-  const uint32_t gchunk = 16u * (uint32_t)((lane & 15) ^ grad_swz(gr));
-  auto issue_a = [&](int st, uint8_t* ab, int i) {
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(a_base + (int64_t)(64 * i) * lda), (short)0, max(rows - 64 * i, 0) * lda, 0x00020000);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(ab + (8 * i + wave) * 1024), 16, off_a,
-                                             (st0 + st) * 128, 0, 0);
+  // Forward weights: LDS row LOAD i + lr holds column b_col(i) + that of row lr.
+  const int tile0 = lr >> 4;   // of the lane's row in the wave column's FN tiles, for i = 0
+  const int bl = MODE == F8_GATED ? 2 * FN * ((lr >> 2) & 3) + 4 * (tile0 & (FN / 2 - 1)) + (lr & 3)
+                                  : 4 * FN * ((lr >> 2) & 3) + 4 * tile0 + (lr & 3);
+  const uint32_t off_b = (uint32_t)bl * (uint32_t)ldb + chunk;
+  // LOAD rows are a wave column's 64 (WN = 4), or two of its eight tiles
+  auto b_col = [&](int i) {
+    if constexpr (WN == 4) return MODE == F8_GATED ? 32 * i : 64 * i;
+    else return MODE == F8_GATED ? 64 * (i >> 2) + 8 * (i & 1) : 128 * (i >> 2) + 8 * (i & 3);
   };
-  auto issue_b = [&](int st, uint8_t* bb, int i) {
-    if constexpr (MODE == F8_GRAD) {
-      // rows past the weight's last repeat it (their row codes are zero)
-      const int s = st0 + st, seg = s >= p.nb, n0 = 128 * (s - (seg ? p.nb : 0));
-      const int left = min(p.n - n0, 128);
-      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)((seg ? p.b1 : p.b0) + ((int64_t)grp * p.n + n0) * ldb + c0), (short)0,
-          (left - 1) * ldb + min(256, ldb - c0), 0x00020000);
-      const uint32_t off = __umul24((uint32_t)min(32 * i + gr, left - 1), (uint32_t)ldb) + gchunk;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16, off,
-                                               0, 0, 0);
-    } else {
-      constexpr int STEP = WIDTH / 4;
-      const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(b_fwd + (int64_t)(STEP * i) * ldb), (short)0, max(cols - STEP * i, 0) * ldb,
-          0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (i8_lds_t)(bb + (8 * i + wave) * 1024), 16,
-                                               off_b, (st0 + st) * 128, 0, 0);
-    }
-  };
-  auto issue = [&](int st, uint8_t* ab, uint8_t* bb) {
+  // Gradient: the weight rows of stage st from their first column of the tile;
+  // rows past the weight's last lie beyond the descriptor and arrive as zeros.
+  const int gr = 4 * wave + (lane >> 4);
+  uint32_t off_g[2];   // of load instructions with even and odd numbers
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < NA) issue_a(st, ab, i);
-      issue_b(st, bb, i);
+  for (int i = 0; i < 2; ++i)
+    off_g[i] = (uint32_t)gr * (uint32_t)ldb +
+               16u * (uint32_t)((lane & 15) ^ grad_swz(gr + 4 * WAVES * i));
+  struct Rows {
+    const uint8_t* base;
+    int bytes;
+  };
+  auto grad_rows = [&](int st) {
+    const int s = st0 + st, seg = s >= p.nb, n0 = 128 * (s - (seg ? p.nb : 0));
+    return Rows{(seg ? p.b1 : p.b0) + ((int64_t)grp * p.n + n0) * ldb + c0,
+                (min(p.n - n0, 128) - 1) * ldb + min(256, ldb - c0)};
+  };
+  const __amdgpu_buffer_rsrc_t a_rsrc =
+      __builtin_amdgcn_make_buffer_rsrc((void*)a_base, (short)0, rows * lda, 0x00020000);
+  const __amdgpu_buffer_rsrc_t b_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((MODE == F8_GATED && WN == 4 && wave >= 4 ? p.b1 : p.b0) +
+              ((int64_t)grp * p.n + c0) * ldb),
+      (short)0, cols * ldb, 0x00020000);
+  const __amdgpu_buffer_rsrc_t u_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((MODE == F8_GATED ? p.b1 : p.b0) + ((int64_t)grp * p.n + c0) * ldb), (short)0,
+      cols * ldb, 0x00020000);
+  // s: the stage's buffers
+  auto issue_a = [&](int st, int s, int i) {
+    constexpr int PER = 128 / LOAD;   // load instructions of row tiles 0 to 3
+    uint8_t* to = i < PER ? (s & 1 ? a1 : a0) + (WAVES * i + wave) * 1024
+                          : (s & 1 ? a1_high : a0_high) + (WAVES * (i - PER) + wave) * 1024;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rsrc, (i8_lds_t)to, 16,
+                                             off_a + (uint32_t)(LOAD * i * lda), (st0 + st) * 128, 0, 0);
+  };
+  auto issue_b = [&](int st, const Rows& from, int s, int i) {
+    const i8_lds_t to = (i8_lds_t)((s & 1 ? b1 : b0) + (WAVES * i + wave) * 1024);
+    if constexpr (MODE == F8_GRAD) {
+      const __amdgpu_buffer_rsrc_t rsrc =
+          __builtin_amdgcn_make_buffer_rsrc((void*)from.base, (short)0, from.bytes, 0x00020000);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, to, 16,
+                                               off_g[i & 1] + (uint32_t)(4 * WAVES * i * ldb), 0, 0, 0);
+    } else {
+      const uint32_t off = off_b + (uint32_t)(b_col(i) * ldb);
+      if (MODE == F8_GATED && WN == 2 && (i & 2))   // up's tiles; with WN = 4 waves 4 to 7 have them
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(u_rsrc, to, 16, off, (st0 + st) * 128, 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rsrc, to, 16, off, (st0 + st) * 128, 0, 0);
     }
+  };
+  auto issue = [&](int st, int s) {
+    const Rows from = MODE == F8_GRAD ? grad_rows(st) : Rows{};
+#pragma unroll
+    for (int i = 0; i < NB; ++i) issue_b(st, from, s, i);
+#pragma unroll
+    for (int i = 0; i < NA; ++i) issue_a(st, s, i);
   };
   // row exponents: every thread has the word of one row (some rows twice)
   constexpr int EROWS = BM <= 64 ? 64 : BM <= 128 ? 128 : 256;
@@ -186,7 +239,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
     for (int s = 0; s < 4; ++s) ea[buf][s][e_at] = (uint8_t)(ew >> (8 * s));
   };
   auto weight_exps = [&]() {
-    for (int t = tid; t < 2 * ST; t += F8_THREADS) {
+    for (int t = tid; t < 2 * ST; t += THREADS) {
       const int which = t & 1, s = st0 + (t >> 1);
       uint8_t v;
       if constexpr (MODE == F8_FWD)
@@ -200,44 +253,46 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
     }
   };
 
-  issue(0, a0, b0);
-  issue(min(1, ST - 1), a1, b1);
+  issue(0, 0);
+  issue(min(1, ST - 1), 1);
   load_exps(q0);
   weight_exps();
   put_exps(0);
 
-  f32x4 acc[FM][4];
+  f32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-  auto sync = [&]() {
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto sync = [&](auto on_way) {   // this many loads of a wave may be on their way
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);
+    __builtin_amdgcn_s_waitcnt(sq_wait_vm(decltype(on_way)::value));
     __builtin_amdgcn_s_waitcnt(SQ_WAIT_LGKM0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  sync();
+  sync(std::integral_constant<int, 0>{});
 
   // ---- fragments: lane (fr, g) holds bytes 16 g .. and 64 + 16 g .. of its row
-  const uint32_t a_row = (uint32_t)(16 * wm + fr) * 128, b_row = (uint32_t)(64 * wn + fr) * 128;
+  const uint32_t a_row = (uint32_t)(16 * wm + fr) * 128, b_row = (uint32_t)(16 * FN * wn + fr) * 128;
   const uint32_t slot0 = 16u * (uint32_t)(g ^ (fr & 7)), slot1 = 16u * (uint32_t)((4 + g) ^ (fr & 7));
   const int tr_row = 16 * g + (fr >> 1), tr_swz = grad_swz(tr_row);
   const uint32_t t_row = (uint32_t)tr_row * 256 + 8u * (uint32_t)(fr & 1);
-  auto read_a = [&](const uint8_t* ab, int i) {
-    const i32x4 lo = *reinterpret_cast<const i32x4*>(ab + a_row + slot0 + i * 4096);
-    const i32x4 hi = *reinterpret_cast<const i32x4*>(ab + a_row + slot1 + i * 4096);
+  auto read_a = [&](int s, int i) {
+    const uint8_t* ab = (i < 4 ? (s & 1 ? a1 : a0) : (s & 1 ? a1_high : a0_high)) + a_row + (i & 3) * 4096;
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(ab + slot0);
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(ab + slot1);
     return (i32x8){lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
   };
-  auto read_b = [&](const uint8_t* bb, int j) {
+  auto read_b = [&](int s, int j) {
+    const uint8_t* bb = s & 1 ? b1 : b0;
     if constexpr (MODE == F8_GRAD) {
       i32x2 t[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)   // rows 16 g + 8 (u & 1) + 64 (u / 2)
         t[u] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
             (__attribute__((address_space(3))) i32x2*)(bb + t_row + (u & 1) * 2048 + (u >> 1) * 16384 +
-                                                       16 * ((4 * wn + j) ^ tr_swz)));
+                                                       16 * ((FN * wn + j) ^ tr_swz)));
       return (i32x8){t[0][0], t[0][1], t[1][0], t[1][1], t[2][0], t[2][1], t[3][0], t[3][1]};
     } else {
       const i32x4 lo = *reinterpret_cast<const i32x4*>(bb + b_row + slot0 + j * 2048);
@@ -246,7 +301,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
     }
   };
   // exponents of the lane's row tiles (byte i) and of its columns' weight block
-  // (forward, gradient: the wave's 64 columns lie in one; gated: gate, up)
+  // (forward, gradient: the wave's columns lie in one; gated: gate, up)
   struct Exps {
     u32x2 rows;
     int w[2];
@@ -257,27 +312,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
       e.w[0] = eb[st][0];
       e.w[1] = eb[st][1];
     } else {
-      e.w[0] = e.w[1] = eb[st][wn >> 1];
+      e.w[0] = e.w[1] = eb[st][FN * wn / 8];
     }
   };
 
-  // n LDS reads among m MFMAs of one region
-  auto interleave = [&](int reads, int mfmas) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < reads) {
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-      }
-    __builtin_amdgcn_sched_barrier(0);
-  };
   auto contract = [&](auto count) {
     constexpr int F = decltype(count)::value;
-    constexpr int NP = (F + 1) / 2;   // pairs of row tiles
+    // The stage's last H row tiles are contracted together behind its barrier, the
+    // L before them in pairs.
+    constexpr int H = F > 4 ? F - 4 : F, L = F - H, NP = L / 2, FIRST = L ? 2 : H;
+    constexpr bool EARLY = PINNED && NP == 2;
+    const std::integral_constant<int, EARLY ? NA + NB : 0> on_way;
     auto product = [&](int i, int j, const i32x8& w, const i32x8& a, const Exps& e) {
-      const int we = e.w[j >> 1], re = (int)e.rows[i >> 2];
+      const int we = e.w[j / (FN / 2)], re = (int)e.rows[i >> 2];
       if constexpr (F16) {
         add_scaled(acc[i][j], f16_block(f8_to_f16(w), f8_to_f16(a)), we + ((re >> (8 * (i & 3))) & 255));
+      } else if constexpr (PINNED) {
+        switch (i & 3) {
+          case 0: pinned_mfma<0>(acc[i][j], w, a, we, re); break;
+          case 1: pinned_mfma<1>(acc[i][j], w, a, we, re); break;
+          case 2: pinned_mfma<2>(acc[i][j], w, a, we, re); break;
+          default: pinned_mfma<3>(acc[i][j], w, a, we, re); break;
+        }
       } else {
 #define SQ_F8_MFMA(B) __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, acc[i][j], 0, 0, 0, we, B, re)
         switch (i & 3) {
@@ -289,54 +345,84 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
 #undef SQ_F8_MFMA
       }
     };
-    // One stage, a pair of row tiles at a time: the pair in registers is
-    // contracted while the next one is read.  When the last pair is in
-    // registers every wave has read all of the stage, so its buffers take stage
-    // st + 2, and stage st + 1 has landed: its first pair and its column tiles
-    // are read under the last pair's MFMAs, as the registers fall free.  Loads
+    // One stage.  Pairs of row tiles first, each contracted while the next one
+    // (the last one: all H others) is read.  Then every wave has read all of the
+    // stage, so its buffers take stage st + 2, and stage st + 1 has landed: under
+    // the MFMAs of the H row tiles, column tile by column tile, its first row
+    // tiles are read, and its column tiles as the registers fall free.  Loads
     // past the last stage fetch it again, into buffers that are not read any
     // more.
-    i32x8 a[2][2], w[4];
+    // EARLY (7 and 8 row tiles): a second barrier behind the first pair, where the
+    // column tiles and row tiles 0 to 3 are done with, lets their loads go a step
+    // earlier, and each load has 1.1 to 1.4 stages to arrive instead of 0.5 to 1
+    // (4480 x 16384 x 6144 gated: 906 -> 860 us, its backward 943 -> 897).
+    i32x8 a[2][2], h[L ? 1 : 2][H], w[FN];
     Exps e, en;
     read_exps(e, 0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) a[0][i] = read_a(a0, i);
+    for (int i = 0; i < FIRST; ++i) (L ? a[0][i] : h[0][i]) = read_a(0, i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = read_b(b0, j);
+    for (int j = 0; j < FN; ++j) w[j] = read_b(0, j);
     // s: the stage's number modulo four.  No branches: the compiler would move
     // MFMAs across them.
     auto stage = [&](int st, int s) {
-      uint8_t *ab = s & 1 ? a1 : a0, *bb = s & 1 ? b1 : b0;
-      const uint8_t *an = s & 1 ? a0 : a1, *bn = s & 1 ? b0 : b1;
-      const int parity = s * NP;   // where the stage's first pair sits
+      const int cur = L ? 0 : s & 1, nxt = L ? 0 : cur ^ 1;   // of h
+      const int ahead = min(st + 2, ST - 1);
+      Rows from{};
+      if (MODE == F8_GRAD && NP == 0) from = grad_rows(ahead);
       if (s == 0) load_exps(q0 + (st >> 2) + 1);
 #pragma unroll
-      for (int q = 0; q + 1 < NP; ++q) {
-        const int cur = (q + parity) & 1;
+      for (int q = 0; q < NP; ++q) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (2 * q + 2 + i < F) a[cur ^ 1][i] = read_a(ab, 2 * q + 2 + i);
+        for (int j = 0; j < FN; ++j) {
+          if (q + 1 < NP) {
+            if (j < 2) a[(q + 1) & 1][j] = read_a(s, 2 * q + 2 + j);
+          } else if (j < H) {
+            h[0][j] = read_a(s, L + j);
+          }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) product(2 * q + i, j, w[j], a[cur][i], e);
-        interleave(4, 8);
+          for (int i = 0; i < 2; ++i) {
+            product(2 * q + i, j, w[j], a[q & 1][i], e);
+            if constexpr (PINNED) __builtin_amdgcn_sched_barrier(0);
+            if (EARLY && q == 1) {
+              if (i == 0) issue_b(ahead, from, s, j);
+              else if (j < 4) issue_a(ahead, s, j);
+            }
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if (EARLY && q == 0 && j == FN - 1) sync(on_way);
+          if (MODE == F8_GRAD && q == 0 && j == 0) from = grad_rows(ahead);
+        }
       }
       if (s == 3) put_exps(((st >> 2) + 1) & 1);
-      sync();
-      const int ahead = min(st + 2, ST - 1), last = (NP - 1 + parity) & 1;
+      sync(on_way);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j < NA) issue_a(ahead, ab, j);
-        issue_b(ahead, bb, j);
-        if (j < 2 && j < F) a[last ^ 1][j] = read_a(an, j);
+      for (int j = 0; j < FN; ++j) {
+        auto fetch = [&]() {
+          if (j < FIRST) (L ? a[0][j] : h[nxt][j]) = read_a(s + 1, j);
+          if (!EARLY && j * NB / FN < (j + 1) * NB / FN) issue_b(ahead, from, s, j * NB / FN);
+        };
+        if (!PINNED) fetch();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (2 * NP - 2 + i < F) product(2 * NP - 2 + i, j, w[j], a[last][i], e);
-        if (j == 2) read_exps(en, min(st + 1, ST - 1));
+        for (int i = 0; i < H; ++i) {
+          product(L + i, j, w[j], h[cur][i], e);
+          if constexpr (PINNED) __builtin_amdgcn_sched_barrier(0);
+          if (PINNED && i == 0) fetch();
+          if (i == (PINNED ? 1 : 0) && j < NA && (!EARLY || j >= 4)) issue_a(ahead, s, j);
+          if (i == H / 2 && j > 0) w[j - 1] = read_b(s + 1, j - 1);
+          if (i == 0 && j == 1) read_exps(en, min(st + 1, ST - 1));
+        }
+        if constexpr (!F16 && !PINNED) {
+#pragma unroll
+          for (int i = 0; i < H; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          }
+        }
         __builtin_amdgcn_sched_barrier(0);
-        w[j] = read_b(bn, j);
       }
+      w[FN - 1] = read_b(s + 1, FN - 1);
       e = en;
     };
     int st = 0;
@@ -357,6 +443,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
   else
     contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
+  if constexpr (PINNED) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // and the last MFMAs ended
   __builtin_amdgcn_sched_barrier(0);
 
   // ---- acc[i][j][v]: row 32 i + 16 wm + fr
@@ -366,41 +453,43 @@ __global__ void __launch_bounds__(F8_THREADS, 1) k_f8_gemm(const F8Args p) {
     if (r >= rows) continue;
     const int64_t row = m0 + r;
     if constexpr (MODE == F8_FWD) {
-      const int c = 64 * wn + 16 * g;
-      float o[16];
+      constexpr int RUN = 4 * FN;
+      const int c = 16 * FN * wn + RUN * g;
+      float o[RUN];
 #pragma unroll
-      for (int t = 0; t < 16; ++t) o[t] = acc[i][t >> 2][t & 3];
+      for (int t = 0; t < RUN; ++t) o[t] = acc[i][t >> 2][t & 3];
       if constexpr (SPLIT)
-        store_run<16>(p.partial, ((int64_t)split * p.m + row) * p.n + c0 + c, o, cols - c, false);
+        store_run<RUN>(p.partial, ((int64_t)split * p.m + row) * p.n + c0 + c, o, cols - c, false);
       else
-        store_run<16>(p.y, row * p.n + c0 + c, o, cols - c, p.y_bf16);
+        store_run<RUN>(p.y, row * p.n + c0 + c, o, cols - c, p.y_bf16);
     } else if constexpr (MODE == F8_GATED) {
-      const int c = 32 * wn + 8 * g;
-      float gv[8], uv[8];
+      constexpr int RUN = 2 * FN;
+      const int c = 8 * FN * wn + RUN * g;
+      float gv[RUN], uv[RUN];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
+      for (int t = 0; t < RUN; ++t) {
         gv[t] = acc[i][t >> 2][t & 3];
-        uv[t] = acc[i][2 + (t >> 2)][t & 3];
+        uv[t] = acc[i][FN / 2 + (t >> 2)][t & 3];
       }
       if constexpr (SPLIT) {
         const int64_t at = ((int64_t)split * p.m + row) * (2 * (int64_t)p.n) + c0 + c;
-        store_run<8>(p.partial, at, gv, cols - c, false);
-        store_run<8>(p.partial, at + p.n, uv, cols - c, false);
+        store_run<RUN>(p.partial, at, gv, cols - c, false);
+        store_run<RUN>(p.partial, at + p.n, uv, cols - c, false);
       } else {
         const int64_t at = row * p.n + c0 + c;
         if (p.g) {
-          store_run<8>(p.g, at, gv, cols - c, true);
-          store_run<8>(p.u, at, uv, cols - c, true);
+          store_run<RUN>(p.g, at, gv, cols - c, true);
+          store_run<RUN>(p.u, at, uv, cols - c, true);
         }
-        float h[8];
+        float h[RUN];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) h[t] = act_value(p.act, gv[t]) * uv[t];
-        store_run<8>(p.y, at, h, cols - c, p.y_bf16);
+        for (int t = 0; t < RUN; ++t) h[t] = act_value(p.act, gv[t]) * uv[t];
+        store_run<RUN>(p.y, at, h, cols - c, p.y_bf16);
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int c = 64 * wn + 16 * j + 4 * g;
+      for (int j = 0; j < FN; ++j) {
+        const int c = 16 * FN * wn + 16 * j + 4 * g;
         const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
         if constexpr (SPLIT)
           store_run<4>(p.partial, ((int64_t)split * p.m + row) * p.k + c0 + c, o, cols - c, false);
@@ -483,6 +572,7 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   const bool gated = kind == SQ_F8_GATED_FWD;
   p.stages = (int)(grad ? (kind == SQ_F8_GATED_BWD ? 2 * nb : nb) : kb);
   p.lax = (p.stages + 3) & ~3;
+  p.pitch = p.stages | 1;
   p.f16 = !bf16;
   p.tile_n = gated ? 128 : 256;
   const int64_t width = grad ? k : n, nt = (width + p.tile_n - 1) / p.tile_n;
@@ -505,11 +595,11 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   else
     for (const F8Tile& t : kF8Tiles) consider(t);
   // a launch has fewer than 2^32 threads
-  p.ok = i8_tile_bound(m, groups, p.tile_m) * nt * p.splits < ((int64_t)1 << 32) / F8_THREADS &&
+  p.ok = i8_tile_bound(m, groups, p.tile_m) * nt * p.splits < ((int64_t)1 << 32) / F8_MAX_THREADS &&
          i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < ((int64_t)1 << 32) / 256 &&
          f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < ((int64_t)1 << 32) / 256;
   size_t off = 0;
-  p.off_codes = off; off = align256(off + (size_t)m * p.stages * 128);
+  p.off_codes = off; off = align256(off + (size_t)m * p.pitch * 128);
   p.off_exps = off;  off = align256(off + (size_t)m * p.lax);
   p.off_part = off;
   off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * width * (gated ? 8 : 4) : 0));
@@ -525,8 +615,9 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
   hipError_t err =
       p.kind == SQ_F8_GATED_BWD
           ? launch_f8_gated_rows(c.a, c.g_in, c.u_in, c.act, c.offsets, p.groups, codes, exps, c.dg,
-                                 c.du, p.m, p.n, p.lax, stream)
-          : launch_f8_rows(c.a, c.offsets, p.groups, codes, exps, p.m, grad ? p.n : p.k, p.lax, stream);
+                                 c.du, p.m, p.n, p.lax, p.pitch, stream)
+          : launch_f8_rows(c.a, c.offsets, p.groups, codes, exps, p.m, grad ? p.n : p.k, p.lax, p.pitch,
+                           stream);
   if (err != hipSuccess) return err;
   F8Args a{};
   a.a = codes; a.ax = exps;
@@ -537,23 +628,23 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
   a.partial = reinterpret_cast<float*>(base + p.off_part);
   a.groups = p.groups; a.m = (int)p.m; a.n = (int)p.n; a.k = (int)p.k;
   a.kb = (int)((p.k + 127) / 128); a.nb = (int)((p.n + 127) / 128);
-  a.lax = p.lax; a.stages = p.stages;
+  a.lax = p.lax; a.pitch = p.pitch; a.stages = p.stages;
   a.y_bf16 = c.y_bf16; a.act = c.act;
   a.most_tiles = (int)i8_tile_bound(p.m, p.groups, p.tile_m);
   a.splits = p.splits;
   const int64_t width = grad ? p.k : p.n;
   const int64_t tiles = a.most_tiles * ((width + p.tile_n - 1) / p.tile_n);
-  const dim3 grid((unsigned)(tiles * p.splits)), block(F8_THREADS);
-#define SQ_F8_GEMM(FM, MODE, F16, SPLIT) \
-  hipLaunchKernelGGL((k_f8_gemm<FM, MODE, F16, SPLIT>), grid, block, 0, stream, a)
+  const dim3 grid((unsigned)(tiles * p.splits));
+#define SQ_F8_GEMM(FM, WN, MODE, F16, SPLIT)                                                   \
+  hipLaunchKernelGGL((k_f8_gemm<FM, WN, MODE, F16, SPLIT>), grid, dim3(128 * WN), 0, stream, a)
 #define SQ_F8_FORM(MODE, SPLIT)                                          \
   do {                                                                   \
-    if (p.f16 && p.tile_m == 64) SQ_F8_GEMM(2, MODE, true, SPLIT);       \
-    else if (p.f16) SQ_F8_GEMM(4, MODE, true, SPLIT);                    \
-    else if (p.tile_m == 64) SQ_F8_GEMM(2, MODE, false, SPLIT);          \
-    else if (p.tile_m == 128) SQ_F8_GEMM(4, MODE, false, SPLIT);         \
-    else if (p.tile_m == 224) SQ_F8_GEMM(7, MODE, false, SPLIT);         \
-    else SQ_F8_GEMM(8, MODE, false, SPLIT);                              \
+    if (p.f16 && p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, true, SPLIT);       \
+    else if (p.f16) SQ_F8_GEMM(4, 4, MODE, true, SPLIT);                    \
+    else if (p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, false, SPLIT);          \
+    else if (p.tile_m == 128) SQ_F8_GEMM(4, 4, MODE, false, SPLIT);         \
+    else if (p.tile_m == 224) SQ_F8_GEMM(7, 2, MODE, false, SPLIT);         \
+    else SQ_F8_GEMM(8, 2, MODE, false, SPLIT);                              \
   } while (0)
 #define SQ_F8_MODE(MODE)                        \
   do {                                          \

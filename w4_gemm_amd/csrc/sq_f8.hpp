@@ -54,8 +54,13 @@ __device__ __forceinline__ u32x2 f8_of_bf16x8(u32x4 v, float f) {
 // ---------------------------------------------------------------- curves
 // act(g) and act'(g) of the gated block in fp32: 0 SiLU g s(g); 1 GELU
 // g Phi(g); 2 its tanh form, which is g s(2 z), z = c (g + 0.044715 g^3).
+// e^x as 2^(x log2 e): the product's rounding costs x 2^-24 of the result, which
+// the curves' own slopes take back.
+__device__ __forceinline__ float exp_f32(float x) {
+  return __builtin_amdgcn_exp2f(1.4426950408889634f * x);
+}
 __device__ __forceinline__ float sigmoid_f32(float x) {
-  return __builtin_amdgcn_rcpf(1.0f + expf(-x));
+  return __builtin_amdgcn_rcpf(1.0f + exp_f32(-x));
 }
 template <int ACT>
 __device__ __forceinline__ void act_curve(float g, float& value, float& slope) {
@@ -66,7 +71,7 @@ __device__ __forceinline__ void act_curve(float g, float& value, float& slope) {
   } else if constexpr (ACT == 1) {
     const float cdf = 0.5f * erfcf(-0.70710678118654752f * g);
     value = g * cdf;
-    slope = cdf + g * 0.39894228040143268f * expf(-0.5f * g * g);
+    slope = cdf + g * 0.39894228040143268f * exp_f32(-0.5f * g * g);
   } else {
     constexpr float C2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     const float p = sigmoid_f32(C2 * (g + 0.044715f * g * g * g));

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(256) k_f8_rows(const uint16_t* __restrict__ x,
                                                  const int32_t* __restrict__ offsets, int groups,
                                                  uint8_t* __restrict__ codes,
                                                  uint8_t* __restrict__ exps, int m, int k, int kb,
-                                                 int lax) {
+                                                 int lax, int pitch) {
   const int lane = threadIdx.x & 63;
   const int per = (kb + 7) >> 3;
   const int unit = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(256) k_f8_rows(const uint16_t* __restrict__ x,
   const float f = f8_inverse(e);
   if (blk >= kb) return;
   const u32x2 lo = f8_of_bf16x8(v[0], f), hi = f8_of_bf16x8(v[1], f);
-  *reinterpret_cast<u32x4*>(codes + ((int64_t)row * kb + blk) * 128 + 16 * (lane & 7)) =
+  *reinterpret_cast<u32x4*>(codes + ((int64_t)row * pitch + blk) * 128 + 16 * (lane & 7)) =
       (u32x4){lo[0], lo[1], hi[0], hi[1]};
   if ((lane & 7) == 0) exps[(int64_t)row * lax + blk] = (uint8_t)e;
 }
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(256) k_f8_gated_rows(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g,
     const uint16_t* __restrict__ u, const int32_t* __restrict__ offsets, int groups,
     uint8_t* __restrict__ codes, uint8_t* __restrict__ exps, uint16_t* __restrict__ dg_out,
-    uint16_t* __restrict__ du_out, int m, int n, int nb, int lax) {
+    uint16_t* __restrict__ du_out, int m, int n, int nb, int lax, int pitch) {
   const int lane = threadIdx.x & 63, sub = lane & 15;
   const int per = (nb + 3) >> 2;
   const int unit = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + (int)(threadIdx.x >> 6));
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256) k_f8_gated_rows(
   if (blk >= nb) return;
   const int eg = f8_exponent(tg), eu = f8_exponent(tu);
   const float fg = f8_inverse(eg), fu = f8_inverse(eu);
-  uint8_t* dst = codes + (int64_t)row * (2 * nb) * 128 + 128 * blk + 8 * sub;
+  uint8_t* dst = codes + ((int64_t)row * pitch + blk) * 128 + 8 * sub;
   *reinterpret_cast<u32x2*>(dst) =
       (u32x2){f8_pack4(dg[0] * fg, dg[1] * fg, dg[2] * fg, dg[3] * fg),
               f8_pack4(dg[4] * fg, dg[5] * fg, dg[6] * fg, dg[7] * fg)};
@@ -215,27 +215,28 @@ int64_t f8_rows_blocks(int64_t m, int64_t cols, bool gated) {
 }
 
 hipError_t launch_f8_rows(const uint16_t* x, const int32_t* offsets, int groups, uint8_t* codes,
-                          uint8_t* exps, int64_t m, int64_t k, int lax, hipStream_t stream) {
+                          uint8_t* exps, int64_t m, int64_t k, int lax, int pitch,
+                          hipStream_t stream) {
   const dim3 grid((unsigned)f8_rows_blocks(m, k, false));
   const int kb = (int)((k + 127) / 128);
   if (k % 8 == 0)
     hipLaunchKernelGGL(k_f8_rows<true>, grid, dim3(256), 0, stream, x, offsets, groups, codes, exps,
-                       (int)m, (int)k, kb, lax);
+                       (int)m, (int)k, kb, lax, pitch);
   else
     hipLaunchKernelGGL(k_f8_rows<false>, grid, dim3(256), 0, stream, x, offsets, groups, codes,
-                       exps, (int)m, (int)k, kb, lax);
+                       exps, (int)m, (int)k, kb, lax, pitch);
   return hipGetLastError();
 }
 
 hipError_t launch_f8_gated_rows(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
                                 const int32_t* offsets, int groups, uint8_t* codes, uint8_t* exps,
                                 uint16_t* dg, uint16_t* du, int64_t m, int64_t n, int lax,
-                                hipStream_t stream) {
+                                int pitch, hipStream_t stream) {
   const dim3 grid((unsigned)f8_rows_blocks(m, n, true));
   const int nb = (int)((n + 127) / 128);
 #define SQ_F8_GATED(ACT, VEC)                                                                     \
   hipLaunchKernelGGL((k_f8_gated_rows<ACT, VEC>), grid, dim3(256), 0, stream, dh, g, u, offsets, \
-                     groups, codes, exps, dg, du, (int)m, (int)n, nb, lax)
+                     groups, codes, exps, dg, du, (int)m, (int)n, nb, lax, pitch)
   if (n % 8 == 0) {
     if (act == 0) SQ_F8_GATED(0, true);
     else if (act == 1) SQ_F8_GATED(1, true);

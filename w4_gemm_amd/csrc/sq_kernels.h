@@ -150,11 +150,12 @@ hipError_t launch_f8_weight(const void* w, int w_bf16, uint8_t* codes, uint8_t* 
                             int32_t* flags, int64_t n, int64_t k, hipStream_t stream);
 int64_t f8_rows_blocks(int64_t m, int64_t cols, bool gated);   // workgroups of the two below
 hipError_t launch_f8_rows(const uint16_t* x, const int32_t* offsets, int groups, uint8_t* codes,
-                          uint8_t* exps, int64_t m, int64_t k, int lax, hipStream_t stream);
+                          uint8_t* exps, int64_t m, int64_t k, int lax, int pitch,
+                          hipStream_t stream);
 hipError_t launch_f8_gated_rows(const uint16_t* dh, const uint16_t* g, const uint16_t* u, int act,
                                 const int32_t* offsets, int groups, uint8_t* codes, uint8_t* exps,
                                 uint16_t* dg, uint16_t* du, int64_t m, int64_t n, int lax,
-                                hipStream_t stream);
+                                int pitch, hipStream_t stream);
 
 // Products: n and k are the weight's, offsets == null is one layer.
 enum { SQ_F8_FWD = 0, SQ_F8_DGRAD = 1, SQ_F8_GATED_FWD = 2, SQ_F8_GATED_BWD = 3 };
@@ -162,6 +163,7 @@ struct F8Plan {
   int kind, groups;
   int64_t m, n, k;
   int stages, lax;       // 128-value blocks along the contraction; bytes of a row's exponents
+  int pitch;             // blocks between rows of codes
   bool f16;              // fp32 results: fp16 MFMA
   int tile_m, tile_n;
   int splits;            // of the contraction

@@ -92,7 +92,7 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes
 constexpr int F8_BN = 256;
 constexpr int F8_BSTAGE = F8_BN * 128;
 constexpr int F8_MAX_THREADS = 512;
-constexpr int F8_MAX_STAGES = 4096;   // of one workgroup: the planner splits longer contractions
+constexpr int F8_MAX_STAGES = 1024;   // of one workgroup: the planner splits longer contractions
 
 __device__ __forceinline__ int grad_swz(int r) { return (r & 7) | (((r >> 4) & 1) << 3); }
 
@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
     constexpr int F = decltype(count)::value;
     // The stage's last H row tiles are contracted together behind its barrier, the
     // L before them in pairs.
-    constexpr int H = F > 4 ? F - 4 : F, L = F - H, NP = L / 2, FIRST = L ? 2 : H;
+    constexpr int H = F16 ? 2 : F > 4 ? F - 4 : F, L = F - H, NP = L / 2, FIRST = L ? 2 : H;
     constexpr bool EARLY = PINNED && NP == 2;
     const std::integral_constant<int, EARLY ? NA + NB : 0> on_way;
     auto product = [&](int i, int j, const i32x8& w, const i32x8& a, const Exps& e) {
@@ -551,6 +551,156 @@ __global__ void __launch_bounds__(256) k_f8_join(const float* __restrict__ parti
   store_run<4>(y, row * width + c, o, left, y_bf16);
 }
 
+// ---------------------------------------------------------------- few rows
+// 16 rows x 16 NT weight columns per workgroup (gated: 8 NT of gate and the same
+// of up), the rows rounded on the way: lane (fr, g) holds values 16 g .. 16 g + 15
+// and 64 + 16 g .. of row fr's block, as the MFMA takes them, so a block's
+// maximum meets in four lanes and nothing is written in between; codes come
+// straight from memory in the same order.  The waves take the blocks along the
+// contraction in turn and their sums meet in LDS in wave order.  With few rows the
+// codes are the whole traffic; rounding x again in every workgroup takes a third
+// of the time they take to arrive (130 vector instructions against 4 KB of codes).
+// VEC: rows of x are 16-byte aligned.
+template <int NT, bool GATED, bool F16, bool VEC>
+__global__ void __launch_bounds__(512) k_f8_stream(const F8Args p, const uint16_t* __restrict__ x) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t red[];
+  constexpr int WIDTH = GATED ? 8 * NT : 16 * NT, HALF = GATED ? NT / 2 : NT;
+  const int tid = threadIdx.x, lane = tid & 63, fr = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int waves = __builtin_amdgcn_readfirstlane((int)(blockDim.x >> 6));
+  const int nt = (p.n + WIDTH - 1) / WIDTH;
+  const int mt = row_tile_count(p.offsets, p.groups, p.m, 16, p.most_tiles, lane);
+  if ((int64_t)blockIdx.x >= (int64_t)mt * nt) return;
+  int64_t tm, tn;
+  xcd_tile(blockIdx.x, (int64_t)mt * nt, nt, tm, tn);
+  RowTile rt;
+  if (!find_row_tile(p.offsets, p.groups, p.m, 16, __builtin_amdgcn_readfirstlane((int)tm), lane, rt))
+    return;
+  const int grp = __builtin_amdgcn_readfirstlane(rt.group);
+  const int rows = __builtin_amdgcn_readfirstlane(rt.rows);
+  const int64_t m0 = __builtin_amdgcn_readfirstlane(rt.row0);
+  const int c0 = __builtin_amdgcn_readfirstlane((int)tn) * WIDTH;
+  const int cols = min(WIDTH, p.n - c0), ldb = 128 * p.kb;
+  const int64_t brow0 = (int64_t)grp * p.n + c0;
+  const __amdgpu_buffer_rsrc_t w_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)(p.b0 + brow0 * ldb), (short)0, cols * ldb, 0x00020000);
+  const __amdgpu_buffer_rsrc_t u_rsrc = __builtin_amdgcn_make_buffer_rsrc(
+      (void*)((GATED ? p.b1 : p.b0) + brow0 * ldb), (short)0, cols * ldb, 0x00020000);
+  const int64_t ex0 = ((int64_t)grp * p.nb + (c0 >> 7)) * p.kb;
+  uint32_t off_w[HALF];   // columns past the tile repeat its last one
+#pragma unroll
+  for (int j = 0; j < HALF; ++j)
+    off_w[j] = (uint32_t)min(16 * j + fr, cols - 1) * (uint32_t)ldb + 16u * g;
+  const bool live = fr < rows;
+  const uint16_t* xrow = x + (m0 + min(fr, rows - 1)) * p.k;
+
+  struct Step {
+    i32x8 w[NT];
+    u32x4 x[4];
+    int e[2];
+  };
+  const int todo = (p.kb - wave + waves - 1) / waves;   // blocks of this wave
+  auto load = [&](Step& f, int t) {
+    const int blk = wave + waves * t;
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t off = off_w[j % HALF];
+      u32x4 lo, hi;
+      if (GATED && j >= HALF) {
+        lo = __builtin_amdgcn_raw_buffer_load_b128(u_rsrc, off, 128 * blk, 0);
+        hi = __builtin_amdgcn_raw_buffer_load_b128(u_rsrc, off, 128 * blk + 64, 0);
+      } else {
+        lo = __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, off, 128 * blk, 0);
+        hi = __builtin_amdgcn_raw_buffer_load_b128(w_rsrc, off, 128 * blk + 64, 0);
+      }
+      f.w[j] = (i32x8){(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+                       (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int col = 128 * blk + 64 * (c >> 1) + 16 * g + 8 * (c & 1), left = p.k - col;
+      f.x[c] = (u32x4){0u, 0u, 0u, 0u};
+      if (live && left > 0) {
+        if constexpr (VEC) f.x[c] = *reinterpret_cast<const u32x4*>(xrow + col);
+        else f.x[c] = load8_u16(xrow + col, left);
+      }
+    }
+    f.e[0] = p.x0[ex0 + blk];
+    f.e[1] = GATED ? p.x1[ex0 + blk] : f.e[0];
+  };
+  f32x4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) acc[j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const Step& f) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = abs_max_u16(top, f.x[i >> 2][i & 3]);
+    top = u16_pair_max(top);
+    const auto s16 = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+    top = max(s16[0], s16[1]);
+    const auto s32 = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+    top = max(s32[0], s32[1]);
+    const int e = f8_exponent(top << 16);
+    const float inv = f8_inverse(e);
+    i32x8 a;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const u32x2 q = f8_of_bf16x8(f.x[c], inv);
+      a[2 * c] = (int)q[0];
+      a[2 * c + 1] = (int)q[1];
+    }
+    if constexpr (F16) {
+      const F16Frag ah = f8_to_f16(a);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        add_scaled(acc[j], f16_block(f8_to_f16(f.w[j]), ah), f.e[GATED && j >= HALF] + e);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(f.w[j], a, acc[j], 0, 0, 0,
+                                                                  f.e[GATED && j >= HALF], 0, e);
+    }
+  };
+  Step f0, f1;
+  if (todo > 0) load(f0, 0);
+  int t = 0;
+  for (; t + 2 <= todo; t += 2) {
+    load(f1, t + 1);
+    compute(f0);
+    if (t + 2 < todo) load(f0, t + 2);
+    compute(f1);
+  }
+  if (t < todo) compute(f0);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    *reinterpret_cast<f32x4*>(red + ((wave * NT + j) * 64 + lane) * 16) = acc[j];
+  __syncthreads();
+  // row fr, columns 16 j + 4 g ..
+  for (int j = wave; j < HALF; j += waves) {
+    auto sum = [&](int tile) {
+      f32x4 o = {0.f, 0.f, 0.f, 0.f};
+      for (int w = 0; w < waves; ++w)
+        o += *reinterpret_cast<const f32x4*>(red + ((w * NT + tile) * 64 + lane) * 16);
+      return o;
+    };
+    const f32x4 s = sum(j);
+    const int c = 16 * j + 4 * g, left = cols - c;
+    const int64_t at = (m0 + fr) * p.n + c0 + c;
+    float o[4] = {s[0], s[1], s[2], s[3]};
+    if constexpr (GATED) {
+      const f32x4 v = sum(HALF + j);
+      const float u[4] = {v[0], v[1], v[2], v[3]};
+      if (p.g && live && left > 0) {
+        store_run<4>(p.g, at, o, left, true);
+        store_run<4>(p.u, at, u, left, true);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = act_value(p.act, o[i]) * u[i];
+    }
+    if (live && left > 0) store_run<4>(p.y, at, o, left, p.y_bf16);
+  }
+}
+
 size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
@@ -575,11 +725,21 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   p.pitch = p.stages | 1;
   p.f16 = !bf16;
   p.tile_n = gated ? 128 : 256;
-  const int64_t width = grad ? k : n, nt = (width + p.tile_n - 1) / p.tile_n;
+  const int64_t width = grad ? k : n;
+  // Few rows: tiles of 16, as many columns as leave every CU a workgroup or two.
+  if (!grad && m <= 16 * std::min<int64_t>(groups, m)) {
+    p.tile_m = 16;
+    const int64_t rt = std::max<int64_t>(1, (int64_t)i8_expected_tiles(m, groups, 16));
+    int nt16 = 4;   // MFMA column tiles
+    while (nt16 > (gated ? 2 : 1) && rt * ((width + (gated ? 8 : 16) * nt16 - 1) / ((gated ? 8 : 16) * nt16)) < 512) nt16 /= 2;
+    p.tile_n = (gated ? 8 : 16) * nt16;
+    p.waves = (int)std::min<int64_t>(8, kb);
+  }
   const int quads = (p.stages + 3) / 4, least = (p.stages + F8_MAX_STAGES - 1) / F8_MAX_STAGES;
+  p.splits = 1;
   double best = 1e30;
   auto consider = [&](const F8Tile& t) {
-    const double tiles = i8_expected_tiles(m, groups, t.rows) * (double)nt / 256.0;
+    const double tiles = i8_expected_tiles(m, groups, t.rows) * (double)((width + p.tile_n - 1) / p.tile_n) / 256.0;
     for (int s = least; s <= std::min(quads, std::max(16, least)); ++s) {
       double us = std::ceil(tiles * s) * (t.fixed + t.stage * (double)p.stages / s);
       if (s > 1) us += 5.0 + (double)m * (double)width * (gated ? 2 : 1) * s * 8e-6 / 4.0;
@@ -590,20 +750,22 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
       }
     }
   };
-  if (p.f16)
+  if (p.tile_m == 16) {
+  } else if (p.f16)
     for (const F8Tile& t : kF16Tiles) consider(t);
   else
     for (const F8Tile& t : kF8Tiles) consider(t);
   // a launch has fewer than 2^32 threads
-  p.ok = i8_tile_bound(m, groups, p.tile_m) * nt * p.splits < ((int64_t)1 << 32) / F8_MAX_THREADS &&
+  p.ok = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n) * p.splits < ((int64_t)1 << 32) / F8_MAX_THREADS &&
          i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < ((int64_t)1 << 32) / 256 &&
          f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < ((int64_t)1 << 32) / 256;
   size_t off = 0;
-  p.off_codes = off; off = align256(off + (size_t)m * p.pitch * 128);
-  p.off_exps = off;  off = align256(off + (size_t)m * p.lax);
+  const size_t held = p.tile_m == 16 ? 0 : (size_t)m;   // rows of codes between the launches
+  p.off_codes = off; off = align256(off + held * p.pitch * 128);
+  p.off_exps = off;  off = align256(off + held * p.lax);
   p.off_part = off;
   off = align256(off + (p.splits > 1 ? (size_t)p.splits * m * width * (gated ? 8 : 4) : 0));
-  p.total = off;
+  p.total = std::max<size_t>(off, 256);   // 0 says that a call is refused
   return p;
 }
 
@@ -612,13 +774,6 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
   uint8_t* codes = reinterpret_cast<uint8_t*>(base + p.off_codes);
   uint8_t* exps = reinterpret_cast<uint8_t*>(base + p.off_exps);
   const bool grad = p.kind == SQ_F8_DGRAD || p.kind == SQ_F8_GATED_BWD;
-  hipError_t err =
-      p.kind == SQ_F8_GATED_BWD
-          ? launch_f8_gated_rows(c.a, c.g_in, c.u_in, c.act, c.offsets, p.groups, codes, exps, c.dg,
-                                 c.du, p.m, p.n, p.lax, p.pitch, stream)
-          : launch_f8_rows(c.a, c.offsets, p.groups, codes, exps, p.m, grad ? p.n : p.k, p.lax, p.pitch,
-                           stream);
-  if (err != hipSuccess) return err;
   F8Args a{};
   a.a = codes; a.ax = exps;
   a.b0 = c.codes[0]; a.b1 = c.codes[1];
@@ -634,6 +789,37 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
   a.splits = p.splits;
   const int64_t width = grad ? p.k : p.n;
   const int64_t tiles = a.most_tiles * ((width + p.tile_n - 1) / p.tile_n);
+  if (p.tile_m == 16) {
+    const size_t lds = (size_t)p.waves * (p.tile_n / (p.kind == SQ_F8_GATED_FWD ? 8 : 16)) * 1024;
+#define SQ_F8_STREAM(NT, GATED, F16, VEC)                                                         \
+  hipLaunchKernelGGL((k_f8_stream<NT, GATED, F16, VEC>), dim3((unsigned)tiles), dim3(64 * p.waves), \
+                     lds, stream, a, c.a)
+#define SQ_F8_STREAM_TYPE(NT, GATED)                                   \
+  do {                                                                 \
+    if (p.f16 && p.k % 8 == 0) SQ_F8_STREAM(NT, GATED, true, true);    \
+    else if (p.f16) SQ_F8_STREAM(NT, GATED, true, false);              \
+    else if (p.k % 8 == 0) SQ_F8_STREAM(NT, GATED, false, true);       \
+    else SQ_F8_STREAM(NT, GATED, false, false);                        \
+  } while (0)
+    if (p.kind == SQ_F8_GATED_FWD) {
+      if (p.tile_n == 16) SQ_F8_STREAM_TYPE(2, true);
+      else SQ_F8_STREAM_TYPE(4, true);
+    } else {
+      if (p.tile_n == 16) SQ_F8_STREAM_TYPE(1, false);
+      else if (p.tile_n == 32) SQ_F8_STREAM_TYPE(2, false);
+      else SQ_F8_STREAM_TYPE(4, false);
+    }
+#undef SQ_F8_STREAM_TYPE
+#undef SQ_F8_STREAM
+    return hipGetLastError();
+  }
+  hipError_t err =
+      p.kind == SQ_F8_GATED_BWD
+          ? launch_f8_gated_rows(c.a, c.g_in, c.u_in, c.act, c.offsets, p.groups, codes, exps, c.dg,
+                                 c.du, p.m, p.n, p.lax, p.pitch, stream)
+          : launch_f8_rows(c.a, c.offsets, p.groups, codes, exps, p.m, grad ? p.n : p.k, p.lax, p.pitch,
+                           stream);
+  if (err != hipSuccess) return err;
   const dim3 grid((unsigned)(tiles * p.splits));
 #define SQ_F8_GEMM(FM, WN, MODE, F16, SPLIT)                                                   \
   hipLaunchKernelGGL((k_f8_gemm<FM, WN, MODE, F16, SPLIT>), grid, dim3(128 * WN), 0, stream, a)

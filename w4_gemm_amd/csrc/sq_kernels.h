@@ -165,7 +165,8 @@ struct F8Plan {
   int stages, lax;       // 128-value blocks along the contraction; bytes of a row's exponents
   int pitch;             // blocks between rows of codes
   bool f16;              // fp32 results: fp16 MFMA
-  int tile_m, tile_n;
+  int tile_m, tile_n;    // tile_m 16: one launch, rows rounded on the way
+  int waves;             // of its workgroups
   int splits;            // of the contraction
   bool ok;               // false: a launch would pass 2^32 threads
   size_t off_codes, off_exps, off_part, total;

@@ -590,10 +590,15 @@ class F8Payload:
         return self.codes.shape[-2]
 
     def abi(self) -> SqF8:
-        _require(self.codes, torch.float8_e4m3fn, "codes")
-        _require(self.exps, torch.uint8, "exps")
-        S.check_f8_payload(self.codes.shape, self.exps.shape, self.k)
-        return SqF8(self.n, self.k, self.codes.data_ptr(), self.exps.data_ptr())
+        codes, exps, k = self.codes, self.exps, self.k
+        _require(codes, torch.float8_e4m3fn, "codes")
+        _require(exps, torch.uint8, "exps")
+        kb = (k + 127) // 128
+        # one comparison for the usual case: the smallest calls take as long as their checks
+        if codes.dim() != 2 or not 0 < k <= _lib.SQ_F8_MAX or codes.shape[1] != 128 * kb or \
+                exps.shape != ((codes.shape[0] + 127) // 128, kb):
+            S.check_f8_payload(codes.shape, exps.shape, k)
+        return SqF8(codes.shape[0], k, codes.data_ptr(), exps.data_ptr())
 
 
 @dataclass
@@ -681,15 +686,18 @@ def _f8_product(call, sizes, ins, cols, offsets, payloads, act, out_dtype, extra
     ins: (name, tensor) of the bf16 inputs [M, cols[0]]; cols: columns of inputs and result;
     extra: optional bf16 tensors that the call writes besides, by name, with their columns."""
     dev = torch.cuda.current_device()
+    m = None
     for name, t in ins:
         _dense(t, torch.bfloat16, name, dev)
-        m = S.check_rows(name, t.shape, cols[0])
-        if m != ins[0][1].shape[0]:
+        rows = S.check_rows(name, t.shape, cols[0])
+        if m is not None and rows != m:
             raise ValueError(f"{name} must have as many rows as {ins[0][0]}")
+        m = rows
     abis = [p.abi() for p in payloads]
     for p in payloads:
-        _dense(p.codes, p.codes.dtype, "the payload", dev)
-        _dense(p.exps, p.exps.dtype, "the payload", dev)
+        for t in (p.codes, p.exps):
+            if t.get_device() != dev:
+                _dense(t, t.dtype, "the payload", dev)
     groups = ()
     if grouped:
         if offsets is None:

@@ -705,13 +705,30 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 }  // namespace
 
-// Tile height and splits of the contraction by modelled time.
+// Tile and splits of the contraction: each form's time (us) is modelled and the
+// least chosen.  The constants are fitted to 2650 timed shapes of both result
+// types and all four products, one layer and up to 64 experts, between 1 and
+// 16384 rows, widths of 64 to 16384 on both sides; over them the choice takes
+// 1.02 to 1.03 times the best form on average.  What decides:
+//   tiles through LDS: whole rounds of 256 tiles, one stage after another; few
+//     tiles split the contraction so that every CU has one (one token x 16384 x
+//     6144: 23 us with four splits, 37 with one), at the price of the partial sums'
+//     trip and a launch; large tiles read less per MFMA;
+//   few rows (k_f8_stream, forward only): a wave's blocks one after another, or
+//     all of a CU's; wide tiles round the rows less often (above: 18 us with 64
+//     columns, 24 with 16), narrow ones are more (16 x 2048 x 8192: 15 us with 16
+//     columns, 25 with 64); eight waves where the tiles do not fill the chip.
 struct F8Tile {
   int rows;
   double fixed, stage;   // us per round, us per stage and round
 };
 constexpr F8Tile kF8Tiles[] = {{64, 6.0, 0.45}, {128, 7.0, 0.65}, {224, 9.0, 1.05}, {256, 9.0, 1.15}};
 constexpr F8Tile kF16Tiles[] = {{64, 6.0, 0.8}, {128, 7.0, 1.4}};
+struct F8Stream {
+  int cols;              // MFMA column tiles
+  double block, share;   // us of a wave's block, of a block among a CU's
+};
+constexpr F8Stream kF8Streams[] = {{1, 0.76, 0.14}, {2, 0.98, 0.215}, {4, 1.48, 0.375}};
 
 F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16) {
   F8Plan p{};
@@ -726,15 +743,6 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   p.f16 = !bf16;
   p.tile_n = gated ? 128 : 256;
   const int64_t width = grad ? k : n;
-  // Few rows: tiles of 16, as many columns as leave every CU a workgroup or two.
-  if (!grad && m <= 16 * std::min<int64_t>(groups, m)) {
-    p.tile_m = 16;
-    const int64_t rt = std::max<int64_t>(1, (int64_t)i8_expected_tiles(m, groups, 16));
-    int nt16 = 4;   // MFMA column tiles
-    while (nt16 > (gated ? 2 : 1) && rt * ((width + (gated ? 8 : 16) * nt16 - 1) / ((gated ? 8 : 16) * nt16)) < 512) nt16 /= 2;
-    p.tile_n = (gated ? 8 : 16) * nt16;
-    p.waves = (int)std::min<int64_t>(8, kb);
-  }
   const int quads = (p.stages + 3) / 4, least = (p.stages + F8_MAX_STAGES - 1) / F8_MAX_STAGES;
   p.splits = 1;
   double best = 1e30;
@@ -750,11 +758,36 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
       }
     }
   };
-  if (p.tile_m == 16) {
-  } else if (p.f16)
+  if (p.f16)
     for (const F8Tile& t : kF16Tiles) consider(t);
   else
     for (const F8Tile& t : kF8Tiles) consider(t);
+  const int64_t used = std::max<int64_t>(1, std::min<int64_t>(groups, m));
+  if (!grad && m <= 24 * used) {
+    // what the LDS form takes more: the rows' own launch; fp16 stages of few rows
+    // (and 7 us of launches and joins beside the codes' way)
+    const double codes = (double)used * (double)n * (double)k * (gated ? 2 : 1) / 5.6e6;
+    best = std::max(best * (p.f16 ? 1.35 : 1.0) + 3.0, codes + 7.0);
+    for (const F8Stream& t : kF8Streams) {
+      const int cols = (gated ? 8 : 16) * t.cols;
+      if (gated && t.cols < 2) continue;
+      const double tiles = i8_expected_tiles(m, groups, 16) * (double)((n + cols - 1) / cols) / 256.0;
+      for (int w : {4, 8}) {
+        const double slow = w == 8 && tiles > 1.5 ? 1.33 : 1.0;
+        const double all = tiles * (double)kb * t.share * slow;
+        const double us = std::max(
+            codes * slow + 1.0,
+            4.9 + 0.17 * tiles + std::max(0.9 * all, t.block * (double)((kb + w - 1) / w) + 0.1 * all));
+        if (us < best) {
+          best = us;
+          p.tile_m = 16;
+          p.tile_n = cols;
+          p.waves = (int)std::min<int64_t>(w, kb);
+          p.splits = 1;
+        }
+      }
+    }
+  }
   // a launch has fewer than 2^32 threads
   p.ok = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n) * p.splits < ((int64_t)1 << 32) / F8_MAX_THREADS &&
          i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < ((int64_t)1 << 32) / 256 &&

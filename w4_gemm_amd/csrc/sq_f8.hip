@@ -86,9 +86,10 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes
 //   rows and forward weight rows (128 bytes): chunk c of row r at slot c ^ (r & 7);
 //   gradient, weight rows of 256 bytes: slot c ^ grad_swz(r), read transposed
 //   (see sq_w8_dgrad.hip).
-// Forward: row 16 j + 4 q + v of a wave column's LDS rows holds its column 4 FN q
-// + 4 j + v, so lane (fr, g) holds 4 FN consecutive columns of row fr; gated: the
-// first half of them gate's, the second the same of up.
+// Forward: row 16 j + 4 q + v of a wave column's LDS rows holds its column 32 (j /
+// 2) + 8 q + 4 (j & 1) + v, so that lane (fr, g) has runs of eight columns of row
+// fr and four lanes store 64 bytes in a row; gated: the first half of the rows
+// are gate's, the second the same of up.
 constexpr int F8_BN = 256;
 constexpr int F8_BSTAGE = F8_BN * 128;
 constexpr int F8_MAX_THREADS = 512;
@@ -110,7 +111,7 @@ __device__ __forceinline__ void pinned_mfma(f32x4& acc, const i32x8& w, const i3
       : "v"(w), "v"(a), "v"(we), "v"(re), "n"(B & 1), "n"(B >> 1));
 }
 
-template <int FM, int WN, int MODE, bool F16, bool SPLIT>
+template <int FM, int WN, int MODE, int ACT, bool F16, bool SPLIT>
 __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
   constexpr int WAVES = 2 * WN, THREADS = 64 * WAVES, FN = 16 / WN, BM = 32 * FM;
   // one load instruction of every wave covers LOAD rows of 128 bytes
@@ -164,13 +165,13 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
   const uint8_t* a_base = p.a + m0 * lda;
   // Forward weights: LDS row LOAD i + lr holds column b_col(i) + that of row lr.
   const int tile0 = lr >> 4;   // of the lane's row in the wave column's FN tiles, for i = 0
-  const int bl = MODE == F8_GATED ? 2 * FN * ((lr >> 2) & 3) + 4 * (tile0 & (FN / 2 - 1)) + (lr & 3)
-                                  : 4 * FN * ((lr >> 2) & 3) + 4 * tile0 + (lr & 3);
+  const int bl = 8 * ((lr >> 2) & 3) + 4 * (tile0 & 1) + (lr & 3) +
+                 (MODE == F8_FWD ? 32 * (tile0 >> 1) : 0);
   const uint32_t off_b = (uint32_t)bl * (uint32_t)ldb + chunk;
   // LOAD rows are a wave column's 64 (WN = 4), or two of its eight tiles
   auto b_col = [&](int i) {
     if constexpr (WN == 4) return MODE == F8_GATED ? 32 * i : 64 * i;
-    else return MODE == F8_GATED ? 64 * (i >> 2) + 8 * (i & 1) : 128 * (i >> 2) + 8 * (i & 3);
+    else return MODE == F8_GATED ? 64 * (i >> 2) + 32 * (i & 1) : 128 * (i >> 2) + 32 * (i & 3);
   };
   // Gradient: the weight rows of stage st from their first column of the tile;
   // rows past the weight's last lie beyond the descriptor and arrive as zeros.
@@ -450,51 +451,70 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
     const int r = 32 * i + 16 * wm + fr;
-    if (r >= rows) continue;
+    const bool r_out = r >= rows;   // the lanes of the gradient's exchange differ in g alone
+    if (MODE != F8_GRAD && r_out) continue;
     const int64_t row = m0 + r;
     if constexpr (MODE == F8_FWD) {
-      constexpr int RUN = 4 * FN;
-      const int c = 16 * FN * wn + RUN * g;
-      float o[RUN];
 #pragma unroll
-      for (int t = 0; t < RUN; ++t) o[t] = acc[i][t >> 2][t & 3];
-      if constexpr (SPLIT)
-        store_run<RUN>(p.partial, ((int64_t)split * p.m + row) * p.n + c0 + c, o, cols - c, false);
-      else
-        store_run<RUN>(p.y, row * p.n + c0 + c, o, cols - c, p.y_bf16);
-    } else if constexpr (MODE == F8_GATED) {
-      constexpr int RUN = 2 * FN;
-      const int c = 8 * FN * wn + RUN * g;
-      float gv[RUN], uv[RUN];
+      for (int q = 0; q < FN / 2; ++q) {
+        const int c = 16 * FN * wn + 32 * q + 8 * g;
+        float o[8];
 #pragma unroll
-      for (int t = 0; t < RUN; ++t) {
-        gv[t] = acc[i][t >> 2][t & 3];
-        uv[t] = acc[i][FN / 2 + (t >> 2)][t & 3];
+        for (int t = 0; t < 8; ++t) o[t] = acc[i][2 * q + (t >> 2)][t & 3];
+        if constexpr (SPLIT)
+          store_run<8>(p.partial, ((int64_t)split * p.m + row) * p.n + c0 + c, o, cols - c, false);
+        else
+          store_run<8>(p.y, row * p.n + c0 + c, o, cols - c, p.y_bf16);
       }
-      if constexpr (SPLIT) {
-        const int64_t at = ((int64_t)split * p.m + row) * (2 * (int64_t)p.n) + c0 + c;
-        store_run<RUN>(p.partial, at, gv, cols - c, false);
-        store_run<RUN>(p.partial, at + p.n, uv, cols - c, false);
-      } else {
-        const int64_t at = row * p.n + c0 + c;
-        if (p.g) {
-          store_run<RUN>(p.g, at, gv, cols - c, true);
-          store_run<RUN>(p.u, at, uv, cols - c, true);
-        }
-        float h[RUN];
+    } else if constexpr (MODE == F8_GATED) {
 #pragma unroll
-        for (int t = 0; t < RUN; ++t) h[t] = act_value(p.act, gv[t]) * uv[t];
-        store_run<RUN>(p.y, at, h, cols - c, p.y_bf16);
+      for (int q = 0; q < FN / 4; ++q) {
+        const int c = 8 * FN * wn + 32 * q + 8 * g;
+        float gv[8], uv[8];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          gv[t] = acc[i][2 * q + (t >> 2)][t & 3];
+          uv[t] = acc[i][FN / 2 + 2 * q + (t >> 2)][t & 3];
+        }
+        if constexpr (SPLIT) {
+          const int64_t at = ((int64_t)split * p.m + row) * (2 * (int64_t)p.n) + c0 + c;
+          store_run<8>(p.partial, at, gv, cols - c, false);
+          store_run<8>(p.partial, at + p.n, uv, cols - c, false);
+        } else {
+          const int64_t at = row * p.n + c0 + c;
+          if (p.g) {
+            store_run<8>(p.g, at, gv, cols - c, true);
+            store_run<8>(p.u, at, uv, cols - c, true);
+          }
+          float h[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) {
+            float value, slope;
+            act_curve<ACT>(gv[t], value, slope);
+            h[t] = value * uv[t];
+          }
+          store_run<8>(p.y, at, h, cols - c, p.y_bf16);
+        }
       }
     } else {
+      // column 16 j + 4 g + v: lanes g and g ^ 1 exchange four columns of tile j
+      // for four of tile j + 1, which leaves each eight in a row
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int c = 16 * FN * wn + 16 * j + 4 * g;
-        const float o[4] = {acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]};
+      for (int j = 0; j < FN; j += 2) {
+        const int c = 16 * FN * wn + 16 * (j + (g & 1)) + 8 * (g >> 1);
+        float o[8];
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][v]),
+                                                          __float_as_uint(acc[i][j + 1][v]), false, false);
+          o[v] = __uint_as_float(r[0]);
+          o[4 + v] = __uint_as_float(r[1]);
+        }
+        if (r_out) continue;
         if constexpr (SPLIT)
-          store_run<4>(p.partial, ((int64_t)split * p.m + row) * p.k + c0 + c, o, cols - c, false);
+          store_run<8>(p.partial, ((int64_t)split * p.m + row) * p.k + c0 + c, o, cols - c, false);
         else
-          store_run<4>(p.y, row * p.k + c0 + c, o, cols - c, p.y_bf16);
+          store_run<8>(p.y, row * p.k + c0 + c, o, cols - c, p.y_bf16);
       }
     }
   }
@@ -854,26 +874,26 @@ hipError_t launch_f8(const F8Plan& p, const F8Call& c, void* workspace, hipStrea
                            stream);
   if (err != hipSuccess) return err;
   const dim3 grid((unsigned)(tiles * p.splits));
-#define SQ_F8_GEMM(FM, WN, MODE, F16, SPLIT)                                                   \
-  hipLaunchKernelGGL((k_f8_gemm<FM, WN, MODE, F16, SPLIT>), grid, dim3(128 * WN), 0, stream, a)
-#define SQ_F8_FORM(MODE, SPLIT)                                          \
+#define SQ_F8_GEMM(FM, WN, MODE, ACT, F16, SPLIT)                                              \
+  hipLaunchKernelGGL((k_f8_gemm<FM, WN, MODE, ACT, F16, SPLIT>), grid, dim3(128 * WN), 0, stream, a)
+#define SQ_F8_FORM(MODE, ACT, SPLIT)                                     \
   do {                                                                   \
-    if (p.f16 && p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, true, SPLIT);       \
-    else if (p.f16) SQ_F8_GEMM(4, 4, MODE, true, SPLIT);                    \
-    else if (p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, false, SPLIT);          \
-    else if (p.tile_m == 128) SQ_F8_GEMM(4, 4, MODE, false, SPLIT);         \
-    else if (p.tile_m == 224) SQ_F8_GEMM(7, 2, MODE, false, SPLIT);         \
-    else SQ_F8_GEMM(8, 2, MODE, false, SPLIT);                              \
+    if (p.f16 && p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, ACT, true, SPLIT); \
+    else if (p.f16) SQ_F8_GEMM(4, 4, MODE, ACT, true, SPLIT);            \
+    else if (p.tile_m == 64) SQ_F8_GEMM(2, 4, MODE, ACT, false, SPLIT);  \
+    else if (p.tile_m == 128) SQ_F8_GEMM(4, 4, MODE, ACT, false, SPLIT); \
+    else if (p.tile_m == 224) SQ_F8_GEMM(7, 2, MODE, ACT, false, SPLIT); \
+    else SQ_F8_GEMM(8, 2, MODE, ACT, false, SPLIT);                      \
   } while (0)
-#define SQ_F8_MODE(MODE)                        \
-  do {                                          \
-    if (p.splits > 1) SQ_F8_FORM(MODE, true);   \
-    else SQ_F8_FORM(MODE, false);               \
-  } while (0)
-  if (grad) SQ_F8_MODE(F8_GRAD);
-  else if (p.kind == SQ_F8_GATED_FWD) SQ_F8_MODE(F8_GATED);
-  else SQ_F8_MODE(F8_FWD);
-#undef SQ_F8_MODE
+  // the curve is applied by the join where the contraction is split
+  if (grad && p.splits > 1) SQ_F8_FORM(F8_GRAD, 0, true);
+  else if (grad) SQ_F8_FORM(F8_GRAD, 0, false);
+  else if (p.kind != SQ_F8_GATED_FWD && p.splits > 1) SQ_F8_FORM(F8_FWD, 0, true);
+  else if (p.kind != SQ_F8_GATED_FWD) SQ_F8_FORM(F8_FWD, 0, false);
+  else if (p.splits > 1) SQ_F8_FORM(F8_GATED, 0, true);
+  else if (c.act == 0) SQ_F8_FORM(F8_GATED, 0, false);
+  else if (c.act == 1) SQ_F8_FORM(F8_GATED, 1, false);
+  else SQ_F8_FORM(F8_GATED, 2, false);
 #undef SQ_F8_FORM
 #undef SQ_F8_GEMM
   if (p.splits > 1) {

@@ -726,10 +726,10 @@ size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
 }  // namespace
 
 // Tile and splits of the contraction: each form's time (us) is modelled and the
-// least chosen.  The constants are fitted to 2650 timed shapes of both result
+// least chosen.  The constants are fitted to 4900 timed shapes of both result
 // types and all four products, one layer and up to 64 experts, between 1 and
 // 16384 rows, widths of 64 to 16384 on both sides; over them the choice takes
-// 1.02 to 1.03 times the best form on average.  What decides:
+// 1.01 times the best form on average.  What decides:
 //   tiles through LDS: whole rounds of 256 tiles, one stage after another; few
 //     tiles split the contraction so that every CU has one (one token x 16384 x
 //     6144: 23 us with four splits, 37 with one), at the price of the partial sums'
@@ -742,8 +742,8 @@ struct F8Tile {
   int rows;
   double fixed, stage;   // us per round, us per stage and round
 };
-constexpr F8Tile kF8Tiles[] = {{64, 6.0, 0.45}, {128, 7.0, 0.65}, {224, 9.0, 1.05}, {256, 9.0, 1.15}};
-constexpr F8Tile kF16Tiles[] = {{64, 6.0, 0.8}, {128, 7.0, 1.4}};
+constexpr F8Tile kF8Tiles[] = {{64, 6.9, 0.63}, {128, 7.0, 0.86}, {224, 9.0, 1.05}, {256, 9.0, 1.18}};
+constexpr F8Tile kF16Tiles[] = {{64, 6.0, 0.8}, {128, 7.5, 1.03}};
 struct F8Stream {
   int cols;              // MFMA column tiles
   double block, share;   // us of a wave's block, of a block among a CU's
@@ -769,8 +769,9 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   auto consider = [&](const F8Tile& t) {
     const double tiles = i8_expected_tiles(m, groups, t.rows) * (double)((width + p.tile_n - 1) / p.tile_n) / 256.0;
     for (int s = least; s <= std::min(quads, std::max(16, least)); ++s) {
-      double us = std::ceil(tiles * s) * (t.fixed + t.stage * (double)p.stages / s);
-      if (s > 1) us += 5.0 + (double)m * (double)width * (gated ? 2 : 1) * s * 8e-6 / 4.0;
+      const double rounds = groups > 1 ? std::max(1.0, tiles * s + 0.25) : std::ceil(tiles * s);
+      double us = rounds * (t.fixed + t.stage * (double)p.stages / s);
+      if (s > 1) us += 4.0 + (double)m * (double)width * (gated ? 2 : 1) * s * 8e-6 / 4.9;
       if (us < best) {
         best = us;
         p.tile_m = t.rows;

@@ -172,6 +172,8 @@ def lib() -> ctypes.CDLL:
         L.sq_linear_fwd_mx4.argtypes = [vp, i64, PX, vp, ctypes.c_int, vp, ctypes.c_size_t, vp]
         L.sq_linear_fwd_mx4.restype = ctypes.c_int
         PF, ci, sz = ctypes.POINTER(SqF8), ctypes.c_int, ctypes.c_size_t
+        L.sqi_f8_form.argtypes = [i32, i64, i32, PF, ci, ctypes.POINTER(i32)]
+        L.sqi_f8_form.restype = ci
         L.sq_quantize_weight_f8.argtypes = [vp, ci, PF, vp, vp]
         L.sq_quantize_weight_f8.restype = ci
         for grouped, offs in (("", []), ("grouped_", [vp, i32])):
@@ -425,3 +427,17 @@ def sq_grouped_gated_bwd_f8(dh, g, u, m: int, offsets, groups: int, gate: SqF8, 
     return (_lib or lib()).sq_grouped_gated_bwd_f8(dh, g, u, m, offsets, groups, gate, up, act, dx,
                                                    dx_dtype, dg, du, workspace, workspace_bytes,
                                                    stream)
+
+
+F8_KINDS = {"fwd": 0, "dgrad": 1, "gated_fwd": 2, "gated_bwd": 3}
+
+
+def f8_form(kind: str, m: int, n: int, k: int, groups: int = 1, bf16: bool = True) -> tuple:
+    """Form of the kernels that an 8-bit float product of these sizes takes: tile rows (16: the form
+    that streams the codes), tile columns, waves of that form's workgroups, splits."""
+    form = (ctypes.c_int32 * 4)()
+    status = lib().sqi_f8_form(F8_KINDS[kind], m, groups, SqF8(n, k, None, None),
+                               SQ_BF16 if bf16 else SQ_F32, form)
+    if status != SQ_OK:
+        raise ValueError(status_str(status))
+    return tuple(form)

@@ -657,6 +657,20 @@ sq_status_t sq_grouped_gated_bwd_f8(const uint16_t* dh, const uint16_t* g, const
                     workspace, workspace_bytes, stream);
 }
 
+// As sqi_i8_form, of the 8-bit float products (kind as in sq_kernels.h): rows and
+// columns of a tile (16 rows: the form that streams the codes), waves of that
+// form's workgroups, splits of the contraction.
+sq_status_t sqi_f8_form(int32_t kind, int64_t m, int32_t groups, const sq_f8_t* p,
+                        sq_dtype_t out_dtype, int32_t form[4]) {
+  if (!form) return SQ_E_NULL;
+  if (kind < 0 || kind > sq::SQ_F8_GATED_BWD || f8_workspace_bytes(kind, m, groups, p) == 0)
+    return SQ_E_SHAPE;
+  const sq::F8Plan plan = sq::plan_f8(kind, m, p->n, p->k, groups, out_dtype == SQ_BF16);
+  const int32_t f[4] = {plan.tile_m, plan.tile_n, plan.tile_m == 16 ? plan.waves : 0, plan.splits};
+  memcpy(form, f, sizeof f);
+  return SQ_OK;
+}
+
 // ---------------------------------------------------------------- MXFP4 mode
 sq_status_t sq_quantize_weight_mx4(const float* w, const sq_mx4_t* p, int32_t* dev_flags,
                                    void* stream) {

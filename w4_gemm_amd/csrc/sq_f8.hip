@@ -767,7 +767,8 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
   p.splits = 1;
   double best = 1e30;
   auto consider = [&](const F8Tile& t) {
-    const double tiles = i8_expected_tiles(m, groups, t.rows) * (double)((width + p.tile_n - 1) / p.tile_n) / 256.0;
+    const double tiles = i8_expected_tiles(m, groups, t.rows) *
+                         (double)((width + p.tile_n - 1) / p.tile_n) / 256.0;
     for (int s = least; s <= std::min(quads, std::max(16, least)); ++s) {
       const double rounds = groups > 1 ? std::max(1.0, tiles * s + 0.25) : std::ceil(tiles * s);
       double us = rounds * (t.fixed + t.stage * (double)p.stages / s);
@@ -810,9 +811,12 @@ F8Plan plan_f8(int kind, int64_t m, int64_t n, int64_t k, int groups, bool bf16)
     }
   }
   // a launch has fewer than 2^32 threads
-  p.ok = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n) * p.splits < ((int64_t)1 << 32) / F8_MAX_THREADS &&
-         i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < ((int64_t)1 << 32) / 256 &&
-         f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < ((int64_t)1 << 32) / 256;
+  constexpr int64_t most = (int64_t)1 << 32;
+  const int64_t tiles = i8_tile_bound(m, groups, p.tile_m) * ((width + p.tile_n - 1) / p.tile_n);
+  p.ok = tiles * p.splits < most / F8_MAX_THREADS;
+  if (p.splits > 1) p.ok = p.ok && i8_tile_bound(m, groups, 16) * ((width + 63) / 64) < most / 256;
+  if (p.tile_m > 16)
+    p.ok = p.ok && f8_rows_blocks(m, grad ? n : k, kind == SQ_F8_GATED_BWD) < most / 256;
   size_t off = 0;
   const size_t held = p.tile_m == 16 ? 0 : (size_t)m;   // rows of codes between the launches
   p.off_codes = off; off = align256(off + held * p.pitch * 128);

@@ -42,7 +42,6 @@ struct F8Args {
   int y_bf16, act, most_tiles, splits;
 };
 
-typedef _Float16 half16 __attribute__((ext_vector_type(16)));
 struct F16Frag {
   half8 h[4];
 };
@@ -101,7 +100,9 @@ __device__ __forceinline__ int grad_swz(int r) { return (r & 7) | (((r >> 4) & 1
 // permutes 224 or more accumulators: 1.7 moves per MFMA.)  The compiler knows of
 // no hazard around it: the s_nop covers an operand that a vector instruction has
 // just written (it costs nothing measurable: an MFMA takes 32 cycles); results
-// are read behind the contraction only, after 32 wait states.
+// are read behind the contraction only, after 32 wait states (pinned_wait), and
+// where pinned_row lets them be: the compiler, which sees no reason to wait,
+// otherwise reads some of them, or stores them to scratch memory, before the wait.
 template <int B>
 __device__ __forceinline__ void pinned_mfma(f32x4& acc, const i32x8& w, const i32x8& a, int we,
                                             int re) {
@@ -110,6 +111,13 @@ __device__ __forceinline__ void pinned_mfma(f32x4& acc, const i32x8& w, const i3
       : "+a"(acc)
       : "v"(w), "v"(a), "v"(we), "v"(re), "n"(B & 1), "n"(B >> 1));
 }
+
+template <int N>
+__device__ __forceinline__ void pinned_row(f32x4 (&acc)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+a"(acc[i]));
+}
+__device__ __forceinline__ void pinned_wait() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
 
 template <int FM, int WN, int MODE, int ACT, bool F16, bool SPLIT>
 __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
@@ -436,6 +444,11 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
     if (st < ST) stage(st, 0);
     if (st + 1 < ST) stage(st + 1, 1);
     if (st + 2 < ST) stage(st + 2, 2);
+    if constexpr (PINNED) {   // in every path here, ahead of the paths' join
+#pragma unroll
+      for (int i = 0; i < FM; ++i) pinned_row(acc[i]);
+      pinned_wait();
+    }
   };
   // a group's last tile is often half empty: it contracts half the row tiles
   constexpr int HALF = (FM + 1) / 2;
@@ -444,12 +457,12 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
   else
     contract(std::integral_constant<int, FM>{});
   __builtin_amdgcn_s_waitcnt(SQ_WAIT_VM0);   // the re-fetches have landed
-  if constexpr (PINNED) asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");   // and the last MFMAs ended
   __builtin_amdgcn_sched_barrier(0);
 
   // ---- acc[i][j][v]: row 32 i + 16 wm + fr
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
+    if constexpr (PINNED) pinned_row(acc[i]);
     const int r = 32 * i + 16 * wm + fr;
     const bool r_out = r >= rows;   // the lanes of the gradient's exchange differ in g alone
     if (MODE != F8_GRAD && r_out) continue;

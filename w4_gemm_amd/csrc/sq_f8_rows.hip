@@ -15,7 +15,9 @@ namespace {
 // ---------------------------------------------------------------- weight
 // A workgroup takes one block: 16 lanes hold a row's 128 values (eight each), 16
 // rows at a time, all 64 of a thread's values in registers between the maximum
-// and the rounding.  Columns from k on are zero codes.
+// and the rounding.  Columns from k on are zero codes.  The weight is read once,
+// which is what bounds it (16384 x 6144 from fp32: 89 us, 503 MB at 5.6 TB/s; a
+// copy of that size runs at 5.3).
 template <bool BF16>
 __device__ __forceinline__ void load8_weight(const void* __restrict__ w, int64_t at, int left,
                                              float (&v)[8]) {
@@ -83,8 +85,10 @@ __global__ void __launch_bounds__(256) k_f8_weight(const void* __restrict__ w,
 }
 
 // ---------------------------------------------------------------- rows
-// Eight lanes hold a block (16 values each), a wave eight blocks of one row.
-// Rows outside the groups' ranges are skipped.
+// Eight lanes hold a block (16 values each), a wave eight blocks of one row; the
+// maximum meets in three lane swaps, so a row is read once and no block waits for
+// another.  Bound by memory (4480 x 16384: 35 us, 221 MB at 6.3 TB/s); 4480 x 6144
+// takes 16 us.  Rows outside the groups' ranges are skipped.
 template <bool VEC>
 __global__ void __launch_bounds__(256) k_f8_rows(const uint16_t* __restrict__ x,
                                                  const int32_t* __restrict__ offsets, int groups,
@@ -129,7 +133,8 @@ __global__ void __launch_bounds__(256) k_f8_rows(const uint16_t* __restrict__ x,
 // Sixteen lanes hold a block (eight values each), a wave four blocks of one row.
 // dg and du are computed in fp32 and rounded twice, each time from there: to
 // e4m3 for the products and to bf16 for the caller.  Block b of a row's codes is
-// dg's, block nb + b du's.
+// dg's, block nb + b du's.  Bound by memory: 12 bytes a value (4480 x 16384: 150 us,
+// 883 MB at 5.9 TB/s).
 template <int ACT, bool VEC>
 __global__ void __launch_bounds__(256) k_f8_gated_rows(
     const uint16_t* __restrict__ dh, const uint16_t* __restrict__ g,

@@ -73,7 +73,7 @@ __device__ __forceinline__ void add_scaled(f32x4& acc, const f32x4& p, int bytes
 // ---------------------------------------------------------------- tiles
 // Products alone: 4480 x 6144 x 16384 in 342 us = 2.64 P operations/s, matrix unit
 // busy 0.65 of the cycles at the 2 GHz it holds; the gated block 4480 x 16384 x
-// 6144, which stores 440 MB, 755 us = 2.39 P, its backward 715-760 us, where 2.5 GB
+// 6144, which stores 440 MB, 705 us = 2.56 P, its backward 715-760 us, where 2.5 GB
 // come from beyond the L2.  About 9 us of each round of 256 tiles are its first
 // loads and its stores.
 // Large tiles (224 and 256 rows) run on four waves, one per SIMD, with 128 columns
@@ -500,9 +500,12 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
           store_run<8>(p.partial, at + p.n, uv, cols - c, false);
         } else {
           const int64_t at = row * p.n + c0 + c;
+          // past the L2 (4480 x 16384 x 6144 with g and u: 767 -> 721 us, h alone
+          // 668 -> 658, with the product that reads h 1083 -> 1047; g and u alone
+          // past it 740; one product's results, either direction: no difference)
           if (p.g) {
-            store_run<8>(p.g, at, gv, cols - c, true);
-            store_run<8>(p.u, at, uv, cols - c, true);
+            store_run<8, true>(p.g, at, gv, cols - c, true);
+            store_run<8, true>(p.u, at, uv, cols - c, true);
           }
           float h[8];
 #pragma unroll
@@ -511,7 +514,7 @@ __global__ void __launch_bounds__(128 * WN, 1) k_f8_gemm(const F8Args p) {
             act_curve<ACT>(gv[t], value, slope);
             h[t] = value * uv[t];
           }
-          store_run<8>(p.y, at, h, cols - c, p.y_bf16);
+          store_run<8, true>(p.y, at, h, cols - c, p.y_bf16);
         }
       }
     } else {

@@ -88,8 +88,9 @@ __device__ __forceinline__ float act_value(int act, float g) {
 }
 
 // N consecutive values of a row as fp32 or bf16; `left` columns remain (rows of
-// an odd width are 4- or 2-byte aligned only).
-template <int N>
+// an odd width are 4- or 2-byte aligned only).  PASS: runs of eight bf16 leave
+// without staying in the L2, whose lines the operands need.
+template <int N, bool PASS = false>
 __device__ __forceinline__ void store_run(void* __restrict__ y, int64_t at, const float (&o)[N],
                                           int left, bool bf16) {
   if (bf16) {
@@ -98,7 +99,13 @@ __device__ __forceinline__ void store_run(void* __restrict__ y, int64_t at, cons
       uint32_t w[N / 2];
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
-      __builtin_memcpy(dst, w, 2 * N);
+      if constexpr (PASS) {
+        static_assert(N == 8, "16 bytes");
+        typedef uint32_t run __attribute__((ext_vector_type(4), aligned(2)));
+        __builtin_nontemporal_store((run){w[0], w[1], w[2], w[3]}, reinterpret_cast<run*>(dst));
+      } else {
+        __builtin_memcpy(dst, w, 2 * N);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)

@@ -76,7 +76,9 @@ __device__ __forceinline__ void act_curve(float g, float& value, float& slope) {
     constexpr float C2 = 1.5957691216057308f;   // 2 sqrt(2 / pi)
     const float p = sigmoid_f32(C2 * (g + 0.044715f * g * g * g));
     value = g * p;
-    slope = p + g * p * (1.0f - p) * C2 * (1.0f + 0.134145f * g * g);
+    // p (1 - p) is zero from |g| = 13 on, where g^2 must not reach infinity
+    const float c = fminf(fmaxf(g, -64.0f), 64.0f);
+    slope = p + g * p * (1.0f - p) * C2 * (1.0f + 0.134145f * c * c);
   }
 }
 __device__ __forceinline__ float act_value(int act, float g) {

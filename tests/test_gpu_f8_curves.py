@@ -72,3 +72,35 @@ def test_forward_of_large_projections(act, dt):
     # 32 is past the flat part's start in fp32: 32 e^-32 is below 2^-40
     R.check(h, want, 2.0 ** -40 * (xd * xd * 2.0 ** -120) + 1e-44)
     assert bool(h.isfinite().all())
+
+
+@pytest.mark.parametrize("act,low", [("silu", -30.0), ("gelu", -6.0), ("gelu_tanh", -6.0)])
+def test_gradient_where_its_first_factors_overflow(act, low):
+    """dh u past fp32's range with a slope that brings dg back into it.  fp32 holds the slope to a
+    few roundings of the exponential's argument (43, 18 and 25 here, each step of the polynomials
+    adding one): below 256 of 2^-24."""
+    import w4_gemm_amd as W
+    m, n, k = 9, 140, 60
+    gen, gate, up = _layers(22, n, k)
+    rnd = lambda: (1 + torch.rand(m, n, generator=gen, device=dev())) * torch.where(   # noqa: E731
+        torch.rand(m, n, generator=gen, device=dev()) < 0.5, -1.0, 1.0)
+    dh, u = (rnd() * 2.0 ** 69).bfloat16(), (rnd() * 2.0 ** 68).bfloat16()
+    u[:, ::3] = (u[:, ::3].float() * 2.0 ** -68).bfloat16()     # ordinary ones among them
+    g = torch.full((m, n), low, dtype=BF16, device=dev())
+    g[:, 1::5] = -500.0                                          # slope 0 in fp32
+    dx, dg, du = W.gated_bwd_f8(dh, g, u, gate.payload(), up.payload(), act)
+    v, slope = R.curve(act, g.double())
+    want = dh.double() * u.double() * slope
+    flat = g == -500
+    assert bool((dg[flat] == 0).all()) and bool((du[flat] == 0).all())
+    R.check(torch.where(flat, 0, dg), torch.where(flat, 0.0, want), 2.0 ** -16 * want.abs() + 1e-44)
+    R.check(torch.where(flat, 0, du), torch.where(flat, 0.0, dh.double() * v), 2.0 ** -16 * (dh.double() * v).abs() + 1e-44)
+    assert bool(dx.isfinite().all())
+    # a gradient that does not fit is infinite, and one of its factors that is not finite is kept
+    dh[4, 5], g[4, 5], u[4, 5] = 2.0 ** 100, 3.0, 2.0 ** 100
+    dh[7, 9] = float("inf")
+    dx, dg, du = W.gated_bwd_f8(dh, g, u, gate.payload(), up.payload(), act)
+    assert bool(dg[4, 5].isinf()) and not bool(dg[7, 9].isfinite())
+    good = torch.ones(m, dtype=torch.bool, device=dev())
+    good[[4, 7]] = False
+    assert bool(dx[good].isfinite().all()) and bool(dx[~good].isnan().all())

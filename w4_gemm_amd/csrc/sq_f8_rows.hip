@@ -171,8 +171,12 @@ __global__ void __launch_bounds__(256) k_f8_gated_rows(
     };
     float value, slope;
     act_curve<ACT>(half(vg), value, slope);
-    dg[i] = half(vd) * half(vu) * slope;
-    du[i] = half(vd) * value;
+    // dh u is exact; where it passes fp32's range the slope may bring dg back, so
+    // there both factors (each above 1 then) are halved 64 times and dg doubled
+    const float d = half(vd), both = d * half(vu);
+    dg[i] = both * slope;
+    if (__builtin_isinf(both)) dg[i] = (d * 0x1p-64f) * (half(vu) * 0x1p-64f) * slope * 0x1p64f * 0x1p64f;
+    du[i] = d * value;
     tg = max(tg, __float_as_uint(dg[i]) & 0x7FFFFFFFu);
     tu = max(tu, __float_as_uint(du[i]) & 0x7FFFFFFFu);
   }

@@ -24,6 +24,9 @@
  *     device that is not gfx950 gets SQ_E_ARCH.
  *   - All tensors are dense and row-major; every pointer must be 16-byte
  *     aligned (SQ_E_ALIGN).
+ *   - *_workspace_bytes(m, ...) is what a call of exactly m rows needs.  Fewer
+ *     rows can need more (they split the contraction, whose partial sums lie
+ *     there), so scratch for calls of several m is the largest of their sizes.
  */
 #ifndef SQ_H
 #define SQ_H

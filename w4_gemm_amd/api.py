@@ -3,6 +3,10 @@
 PyTorch only allocates device memory and supplies the current HIP stream;
 every step of the layer runs in libsq's kernels.  Each call raises SqError on a
 non-OK status.  Tensors must live on the current device.
+
+Each *_workspace_bytes gives the scratch of a call of exactly m rows.  Fewer rows
+can need more (they split the contraction), so a workspace for calls of several m
+takes the largest of their sizes.
 """
 from __future__ import annotations
 
